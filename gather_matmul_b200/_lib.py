@@ -23,9 +23,15 @@ LORA_MAX_TOKENS = 1 << 22
 LORA_NOALLOC_MAX_TOKENS = 8192
 LORA_FLAG_PDL_EARLY = 1
 LORA_FLAG_GROUPED = 2
+LORA_FP8_BLOCK = 128
+LORA_MAX_WIDTH = 1 << 20
+LORA_MAX_HEAD_DIM = 256
+LORA_MAX_HEADS = 4096
+ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 # Every symbol the header declares, with (restype, argtypes).
 _i32, _i64, _sz, _f32, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_void_p
+_f64 = ctypes.c_double
 SIGNATURES = {
     "lora_workspace_bytes": (_sz, [_i32, _i32]),
     "lora_workspace_reset": (_i32, [_vp, _sz, _vp]),
@@ -49,6 +55,17 @@ SIGNATURES = {
     "lora_shrink_laned": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp,
                                  _i32, _vp, _sz, _vp]),
     "lora_set_slot_ranks": (_i32, [_i32, _vp, _vp, _sz, _vp]),
+    "lora_quantize_fp8": (_i32, [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "lora_matmul_fp8": (_i32, [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                               _vp]),
+    "lora_linear_fp8_workspace_bytes": (_sz, [_i32, _i32]),
+    "lora_linear_fp8": (_i32, [_i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
+                               _sz, _vp]),
+    "lora_rope_frequencies": (_i32, [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _vp, _vp]),
+    "lora_rope": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                         _vp, _f32, _i32, _vp]),
+    "lora_norm_rope": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _f32, _vp,
+                              _i64, _vp, _vp, _vp, _f32, _i32, _vp]),
     "lora_status_string": (ctypes.c_char_p, [_i32]),
     "lora_build_info": (ctypes.c_char_p, []),
     "lora_launch_count": (ctypes.c_ulonglong, []),

@@ -66,6 +66,42 @@ struct FusedArgs {
   int pdl_early;            // A, B and idx may be read before the previous kernel ends
 };
 
+struct QuantArgs {
+  const void* x;
+  int64_t ldx;
+  void* q;
+  int64_t ldq;
+  float* scale;
+  int T, K, block_rows;
+};
+
+struct MatmulFp8Args {
+  const void* q;
+  int64_t ldq;
+  const float* q_scale;
+  const void* W;
+  int64_t ldw;
+  const float* w_scale;
+  void* y;
+  int64_t ldy;
+  int T, N, K;
+};
+
+struct RopeArgs {
+  const void* x;
+  int64_t ldx;
+  void* y;
+  int64_t ldy;
+  const void* weight[LORA_MAX_SLICES];   // null: no norm of this slice
+  int64_t x_off[LORA_MAX_SLICES], y_off[LORA_MAX_SLICES];
+  int head_end[LORA_MAX_SLICES];         // running total of the slices' heads
+  int n_slices, T, dim, rot;
+  const int64_t* positions;
+  const double* inv_freq;
+  float attn_scale, eps;
+  int interleaved;
+};
+
 // Every kernel launch of the library passes its status through here, so that
 // lora_launch_count() reports how many launches (or stream-capture records)
 // the library has made.
@@ -119,6 +155,10 @@ cudaError_t launch_expand_grouped_tc(lora_dtype dt, const ExpandArgs& a, cudaStr
 // Laned shrink: all slots' A as one [S*r, D] matrix on tensor cores, each
 // token's own lanes selected; needs no grouping.
 cudaError_t launch_shrink_laned(lora_dtype dt, const ShrinkArgs& a, cudaStream_t st);
+cudaError_t launch_quantize_fp8(lora_dtype dt, const QuantArgs& a, cudaStream_t st);
+cudaError_t launch_matmul_fp8(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st);
+// norm: the slices with a weight are normed before the rotation
+cudaError_t launch_rope(lora_dtype dt, const RopeArgs& a, bool norm, cudaStream_t st);
 // Whether the per-token calls use the tensor-core kernels for this shape.
 inline bool grouped_tc_preferred(int T, int r, int S) { return r >= 16 && T >= 16 * S; }
 

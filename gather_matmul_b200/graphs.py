@@ -22,14 +22,15 @@ from . import ops
 
 
 class LoraGraphSet:
-    """Two captured graphs of one step: has_lora False (no LoRA call at all)
+    """Two captured graphs of one step: has_lora False (no adapter call at all)
     and True (the step's LoRA calls recorded).
 
         gs = LoraGraphSet(step).capture()
         gs.replay_for(idx_host, S)     # picks the graph from the batch's indices
 
     step(has_lora) enqueues one step on the current stream; with has_lora
-    False it must enqueue no call of this library.  Inputs and outputs live
+    False it must enqueue no adapter call (base products and rotations are the
+    same in both).  Inputs and outputs live
     in tensors the step closes over, so a replay reads whatever they hold.
     """
 

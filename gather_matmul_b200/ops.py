@@ -12,6 +12,8 @@ and streams.
   bgmv(x, A, B, idx, y, buf, meta, scale)      group + shrink + expand in one call
   shrink_segment / expand_segment              the same with segments
   check_errors(meta)                           device-side bad-index report
+  quantize_fp8 / matmul_fp8 / linear_fp8       the base product y = x W^T in block-scaled e4m3
+  rope / norm_rope / rope_frequencies          rotation (and norms) of q and k head slices
 
 has_active: the per-token calls take the host flag of the C ABI.  Left as
 None, it is derived from `idx_host` (a host copy of the batch's indices, as a
@@ -275,6 +277,192 @@ def shrink_noalloc(x: torch.Tensor, A: Sequence[torch.Tensor], idx: torch.Tensor
         _dtype(x), T, D, r, S, len(A), _ptr(x), ldx, _ptrs(A), _ptr(idx), _ptr(buf),
         int(bool(has_active)), _stream(stream)))
     return buf
+
+
+# ---------------------------------------------------------------------------
+# Around a LoRA-wrapped projection: the 8-bit base product, and the rotation
+# (and norms) of the query and key heads.  Tensors must lie on the current
+# CUDA device.
+# ---------------------------------------------------------------------------
+_FP8 = torch.float8_e4m3fn
+
+
+def _here(*tensors):
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError("tensors must lie on the current CUDA device")
+
+
+def _rows(t, name, dtype=None):
+    """Row stride of a 2-D tensor with unit column stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape[0] > 1:
+        return t.stride(0)
+    # a single row has no next one: any stride that the alignment rules take
+    return -(-max(t.shape[1], 1) // 16) * 16
+
+
+def _scales(t, name, rows, K):
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (rows, -(-K // 128)):
+        raise TypeError(f"{name} must be a contiguous float32 tensor of {rows} x {-(-K // 128)}")
+
+
+def quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1,
+                 stream=None):
+    """q, scale = x in e4m3 with one fp32 scale per group of 128 columns of a
+    row (block_rows=1, activations) or per 128 x 128 block (block_rows=128,
+    weights): scale = max|x| / 448, q = x / scale rounded once.
+
+    x: fp16/bf16 [T, K]; q: float8_e4m3fn [T, K] whose rows start at multiples
+    of 16; scale: float32 [ceil(T / block_rows), ceil(K / 128)]."""
+    ldx, ldq = _rows(x, "x"), _rows(q, "q", _FP8)
+    T, K = x.shape
+    if q.shape != x.shape:
+        raise ValueError("q must have the shape of x")
+    _scales(scale, "scale", -(-T // block_rows) if block_rows > 0 else 0, K)
+    _here(x, q, scale)
+    _check("lora_quantize_fp8", _lib.load().lora_quantize_fp8(
+        _dtype(x), T, K, block_rows, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(),
+        _stream(stream)))
+    return q, scale
+
+
+def matmul_fp8(q: torch.Tensor, q_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+               y: torch.Tensor, stream=None) -> torch.Tensor:
+    """y = (q * q_scale) (W * w_scale)^T: products and sums in fp32, rounded
+    once to y's fp16/bf16.  q, q_scale as quantize_fp8(x, ...) writes them, W
+    [N, K] and w_scale as quantize_fp8(..., block_rows=128) does; y: [T, N]."""
+    ldq, ldw, ldy = _rows(q, "q", _FP8), _rows(W, "W", _FP8), _rows(y, "y")
+    T, K = q.shape
+    N = W.shape[0]
+    if W.shape[1] != K or y.shape[0] != T or y.shape[1] != N:
+        raise ValueError("shapes must be q [T, K], W [N, K], y [T, N]")
+    _scales(q_scale, "q_scale", T, K)
+    _scales(w_scale, "w_scale", -(-N // 128), K)
+    _here(q, q_scale, W, w_scale, y)
+    _check("lora_matmul_fp8", _lib.load().lora_matmul_fp8(
+        _dtype(y), T, N, K, q.data_ptr(), ldq, q_scale.data_ptr(), W.data_ptr(), ldw,
+        w_scale.data_ptr(), y.data_ptr(), ldy, _stream(stream)))
+    return y
+
+
+def linear_fp8_workspace(T: int, K: int, device="cuda") -> torch.Tensor:
+    """A workspace for linear_fp8() of up to T tokens of K columns."""
+    n = _lib.load().lora_linear_fp8_workspace_bytes(int(T), int(K))
+    if n == 0:
+        raise LoraError("lora_linear_fp8_workspace_bytes", _lib.LORA_ERR_UNSUPPORTED)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def linear_fp8(x: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
+               work: torch.Tensor, stream=None) -> torch.Tensor:
+    """y = x (W * w_scale)^T with x quantised per token and 128 columns:
+    quantize_fp8 into the workspace and matmul_fp8 in one call.  x, y:
+    fp16/bf16 [T, K], [T, N] of one dtype; work: linear_fp8_workspace(T, K),
+    one for each stream that such calls run on."""
+    ldx, ldw, ldy = _rows(x, "x"), _rows(W, "W", _FP8), _rows(y, "y", x.dtype)
+    T, K = x.shape
+    N = W.shape[0]
+    if W.shape[1] != K or y.shape[0] != T or y.shape[1] != N:
+        raise ValueError("shapes must be x [T, K], W [N, K], y [T, N]")
+    _scales(w_scale, "w_scale", -(-N // 128), K)
+    if not work.is_contiguous():
+        raise ValueError("work must be contiguous")
+    _here(x, W, w_scale, y, work)
+    _check("lora_linear_fp8", _lib.load().lora_linear_fp8(
+        _dtype(x), T, N, K, x.data_ptr(), ldx, W.data_ptr(), ldw, w_scale.data_ptr(), y.data_ptr(),
+        ldy, work.data_ptr(), work.numel() * work.element_size(), _stream(stream)))
+    return y
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor: float = 1.0,
+                     original_length: float = 0.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq, attn_scale) for rope(): radians per position of the rot / 2
+    pairs (float64 tensor) and the factor on cos and sin.  kind: "none",
+    "linear", "ntk", "yarn" or "bands" (see lora_rope_frequencies)."""
+    if kind not in _lib.ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_lib.ROPE_KINDS)}")
+    out = (ctypes.c_double * max(int(rot) // 2, 1))()
+    attn = ctypes.c_float()
+    _check("lora_rope_frequencies", _lib.load().lora_rope_frequencies(
+        int(rot), float(base), _lib.ROPE_KINDS[kind], float(factor), float(original_length),
+        float(beta_fast), float(beta_slow), out, ctypes.byref(attn)))
+    return torch.tensor(list(out), dtype=torch.float64, device=device), attn.value
+
+
+def _offsets(t, heads, dim, col_off):
+    if col_off is None:
+        col_off, c = [], 0
+        for h in heads:
+            col_off.append(c)
+            c += h * dim
+    if len(col_off) != len(heads):
+        raise ValueError("one column offset per slice")
+    for h, c in zip(heads, col_off):
+        if c + h * dim > t.shape[1]:
+            raise ValueError("a slice's heads reach past the last column")
+    return (ctypes.c_int64 * len(heads))(*col_off)
+
+
+def _rope_common(x, y, heads, positions, inv_freq):
+    ldx, ldy = _rows(x, "x"), _rows(y, "y", x.dtype)
+    T = x.shape[0]
+    if y.shape[0] != T:
+        raise ValueError("x and y must have the same rows")
+    if positions.dtype != torch.int64 or not positions.is_contiguous() or positions.numel() != T:
+        raise TypeError("positions must be a contiguous int64 tensor of one position per token")
+    if inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a contiguous float64 tensor of one frequency per pair")
+    return T, ldx, ldy, (ctypes.c_int32 * len(heads))(*heads)
+
+
+def rope(x: torch.Tensor, y: torch.Tensor, heads: Sequence[int], head_dim: int,
+         positions: torch.Tensor, inv_freq: torch.Tensor, x_col_off=None, y_col_off=None,
+         interleaved: bool = False, attn_scale: float = 1.0, stream=None) -> torch.Tensor:
+    """Rotary positions of head slices: slice i is heads[i] heads of head_dim
+    columns from x_col_off[i] of x, written from y_col_off[i] of y (both side
+    by side from column 0 by default).  The first 2 * len(inv_freq) elements
+    of each head are rotated by positions[t] * inv_freq[pair], pairs split in
+    halves or interleaved; the rest are copied.  y may be x with the same
+    offsets (in place).  positions: int64 [T]; inv_freq, attn_scale from
+    rope_frequencies()."""
+    T, ldx, ldy, h = _rope_common(x, y, heads, positions, inv_freq)
+    _here(x, y, positions, inv_freq)
+    _check("lora_rope", _lib.load().lora_rope(
+        _dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx,
+        _offsets(x, heads, head_dim, x_col_off), y.data_ptr(), ldy,
+        _offsets(y, heads, head_dim, y_col_off), positions.data_ptr(), inv_freq.data_ptr(),
+        attn_scale, bool(interleaved), _stream(stream)))
+    return y
+
+
+def norm_rope(x: torch.Tensor, weights, y: torch.Tensor, heads: Sequence[int], head_dim: int,
+              positions: torch.Tensor, inv_freq: torch.Tensor, eps: float = 1e-6, x_col_off=None,
+              y_col_off=None, interleaved: bool = False, attn_scale: float = 1.0,
+              stream=None) -> torch.Tensor:
+    """rope() with a root-mean-square norm of each head before it, in one
+    pass: weights holds one tensor [head_dim] of x's dtype per slice, or None
+    for a slice without a norm."""
+    T, ldx, ldy, h = _rope_common(x, y, heads, positions, inv_freq)
+    if len(weights) != len(heads):
+        raise ValueError("one weight (or None) per slice")
+    for w in weights:
+        if w is not None and (w.dtype != x.dtype or not w.is_contiguous() or
+                              w.numel() != head_dim):
+            raise TypeError("a weight must be a contiguous tensor of head_dim elements of x's dtype")
+    _here(x, y, positions, inv_freq, *[w for w in weights if w is not None])
+    ws = (ctypes.c_void_p * len(weights))(*[None if w is None else w.data_ptr() for w in weights])
+    _check("lora_norm_rope", _lib.load().lora_norm_rope(
+        _dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx,
+        _offsets(x, heads, head_dim, x_col_off), ws, eps, y.data_ptr(), ldy,
+        _offsets(y, heads, head_dim, y_col_off), positions.data_ptr(), inv_freq.data_ptr(),
+        attn_scale, bool(interleaved), _stream(stream)))
+    return y
 
 
 def check_errors(meta: torch.Tensor, stream=None) -> int:

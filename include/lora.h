@@ -364,6 +364,162 @@ LORA_API lora_status lora_shrink_noalloc(lora_dtype dtype, int T, int D, int r, 
                                          const void* const* A, const int32_t* idx, float* buf,
                                          int has_active, lora_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around a LoRA-wrapped projection: the base product y = x W^T in 8 bits, and
+ * what follows it on the query and key slices of a fused q/k/v projection.
+ *
+ * 8-bit values are e4m3 (sign, 4 exponent bits, 3 mantissa bits, largest
+ * finite value 448, no infinities).  A scale, fp32, belongs to each group of
+ * LORA_FP8_BLOCK = 128 columns of an activation row and to each block of 128
+ * rows x 128 columns of a weight; the last group, or block, of a side that is
+ * no multiple of 128 is smaller.  Nothing is read or written past column K
+ * (or N) of a row, whatever its stride.
+ * ------------------------------------------------------------------------ */
+#define LORA_FP8_BLOCK 128
+#define LORA_MAX_WIDTH (1 << 20)
+
+/*
+ * Quantise 16-bit values to e4m3 with one scale per group of 128 columns
+ * (block_rows = 1, activations) or per 128 x 128 block (block_rows = 128,
+ * weights, once when they are loaded):
+ *
+ *   a        = max(|x| over the group, 2^-100)
+ *   scale    = a / 448, rounded to fp32
+ *   q[t][k]  = x[t][k] * 448 / a, the real quotient rounded once to the
+ *              nearest e4m3 value, ties to even
+ *
+ * so that q * scale is near x.  A group that holds an infinity or a NaN has
+ * the scale infinity or NaN, which turns every output it enters into NaN.
+ *
+ *   x      device [T, ldx] dtype, ldx >= K a multiple of 8.
+ *   q      device [T, ldq] bytes, ldq >= K a multiple of 16.
+ *   scale  device fp32 [ceil(T / block_rows), ceil(K / 128)] contiguous.
+ * 0 <= T <= LORA_MAX_TOKENS, 1 <= K <= LORA_MAX_WIDTH.  One launch.
+ */
+LORA_API lora_status lora_quantize_fp8(lora_dtype dtype, int T, int K, int block_rows,
+                                       const void* x, int64_t ldx, void* q, int64_t ldq,
+                                       float* scale, lora_stream_t stream);
+
+/*
+ * Block-scaled 8-bit matrix product:
+ *
+ *   y[t][n] = round( sum_b q_scale[t][b] * w_scale[n / 128][b]
+ *                    * sum_{k in group b} q[t][k] * W[n][k] )
+ *
+ * with products and sums in fp32 and one rounding to dtype; y is overwritten.
+ *
+ *   q, q_scale   as lora_quantize_fp8 with block_rows = 1 writes them.
+ *   W, w_scale   device [N, ldw] bytes (ldw >= K a multiple of 16) and fp32
+ *                [ceil(N / 128), ceil(K / 128)] contiguous: a weight as
+ *                lora_quantize_fp8 with block_rows = 128 writes it.
+ *   y            device [T, ldy] dtype, ldy >= N a multiple of 8; must not
+ *                overlap the inputs.
+ * 0 <= T <= LORA_MAX_TOKENS, 1 <= N, K <= LORA_MAX_WIDTH.
+ */
+LORA_API lora_status lora_matmul_fp8(lora_dtype dtype, int T, int N, int K, const void* q,
+                                     int64_t ldq, const float* q_scale, const void* W,
+                                     int64_t ldw, const float* w_scale, void* y, int64_t ldy,
+                                     lora_stream_t stream);
+
+/*
+ * The base product of a projection from 16-bit inputs: lora_quantize_fp8 of x
+ * (block_rows = 1) into the workspace, then lora_matmul_fp8, with the same
+ * results.  x, y as there.
+ *
+ *   work   device workspace of at least lora_linear_fp8_workspace_bytes(T, K)
+ *          bytes, 256-byte aligned, overwritten; calls that may run at the
+ *          same time need one each.
+ */
+LORA_API size_t lora_linear_fp8_workspace_bytes(int T, int K);
+LORA_API lora_status lora_linear_fp8(lora_dtype dtype, int T, int N, int K, const void* x,
+                                     int64_t ldx, const void* W, int64_t ldw,
+                                     const float* w_scale, void* y, int64_t ldy, void* work,
+                                     size_t work_bytes, lora_stream_t stream);
+
+/*
+ * Rotary frequencies, computed on the host in fp64: radians per position of
+ * the rot / 2 pairs, f_i = base^(-2 i / rot), changed for contexts longer than
+ * the trained one by `kind`:
+ *
+ *   LORA_ROPE_NONE     f_i
+ *   LORA_ROPE_LINEAR   f_i / factor
+ *   LORA_ROPE_NTK      base * factor^(rot / (rot - 2)) in place of base (rot >= 4)
+ *   LORA_ROPE_YARN     by the turns a pair makes over original_length: f_i
+ *                      from beta_fast turns on, f_i / factor up to beta_slow
+ *                      turns, a linear ramp over the pair index between (its
+ *                      ends rounded outward to whole pairs); attn_scale =
+ *                      0.1 ln(factor) + 1 for factor > 1
+ *   LORA_ROPE_BANDS    by the same turns: f_i from beta_fast on, f_i / factor
+ *                      up to beta_slow, and between them
+ *                      ((1 - u) / factor + u) f_i with
+ *                      u = (turns - beta_slow) / (beta_fast - beta_slow)
+ *
+ *   rot         rotated elements of a head, even, 2 .. LORA_MAX_HEAD_DIM.
+ *   factor      > 0; original_length > 0 and beta_fast > beta_slow > 0 for the
+ *               last two kinds (unused otherwise).
+ *   inv_freq    host fp64 [rot / 2], written.
+ *   attn_scale  host, written: the factor on cos and sin (1 but for YARN).
+ */
+#define LORA_MAX_HEAD_DIM 256
+typedef enum {
+  LORA_ROPE_NONE = 0,
+  LORA_ROPE_LINEAR = 1,
+  LORA_ROPE_NTK = 2,
+  LORA_ROPE_YARN = 3,
+  LORA_ROPE_BANDS = 4
+} lora_rope_kind;
+LORA_API lora_status lora_rope_frequencies(int rot, double base, lora_rope_kind kind,
+                                           double factor, double original_length,
+                                           double beta_fast, double beta_slow,
+                                           double* inv_freq, float* attn_scale);
+
+/*
+ * Rotary positions on the head slices of a fused projection, one launch.  For
+ * every head of every slice the pair (a, b) = (x[i], x[i + rot / 2]), or
+ * (x[2 i], x[2 i + 1]) when interleaved, becomes
+ *
+ *   attn_scale * (a cos - b sin),  attn_scale * (b cos + a sin)
+ *
+ * at the angle positions[t] * inv_freq[i] (formed and reduced in fp64, so far
+ * positions lose nothing); elements rot .. head_dim - 1 are copied.
+ *
+ *   heads       host int32 [n_slices], heads of each slice, side by side from
+ *               column x_col_off[i] of x (and y_col_off[i] of y).
+ *   x, y        device [T, ldx], [T, ldy] dtype.  y may be x with ldy = ldx
+ *               and equal offsets (in place); otherwise the slices read and
+ *               written must not share memory (checked).  Columns of y
+ *               outside the slices are left as they were.
+ *   positions   device int64 [T], of any sign; |position| < 2^53.
+ *   inv_freq    device fp64 [rot / 2], 8-byte aligned.
+ * head_dim a multiple of 8 up to LORA_MAX_HEAD_DIM, rot even, 2 .. head_dim;
+ * at most LORA_MAX_HEADS heads in all.
+ */
+#define LORA_MAX_HEADS 4096
+LORA_API lora_status lora_rope(lora_dtype dtype, int T, int head_dim, int rot, int n_slices,
+                               const int32_t* heads, const void* x, int64_t ldx,
+                               const int64_t* x_col_off, void* y, int64_t ldy,
+                               const int64_t* y_col_off, const int64_t* positions,
+                               const double* inv_freq, float attn_scale, int interleaved,
+                               lora_stream_t stream);
+
+/*
+ * lora_rope with a root-mean-square norm of each head before it, in the same
+ * pass: n[e] = x[e] * w_i[e] / sqrt(mean(x^2) + eps) over the head_dim
+ * elements of the head (all of them, rotated or not), in fp32; the result is
+ * rounded once, after the rotation.
+ *
+ *   weight   host array of n_slices device pointers to dtype [head_dim],
+ *            16-byte aligned; a null entry leaves that slice without a norm
+ *            (rotation only).
+ *   eps      finite, > 0.
+ */
+LORA_API lora_status lora_norm_rope(lora_dtype dtype, int T, int head_dim, int rot, int n_slices,
+                                    const int32_t* heads, const void* x, int64_t ldx,
+                                    const int64_t* x_col_off, const void* const* weight,
+                                    float eps, void* y, int64_t ldy, const int64_t* y_col_off,
+                                    const int64_t* positions, const double* inv_freq,
+                                    float attn_scale, int interleaved, lora_stream_t stream);
+
 /* Static, human-readable name of a status. */
 LORA_API const char* lora_status_string(lora_status status);
 
