@@ -29,7 +29,8 @@ lora_status check_sizes(lora_dtype dt, int T, int n, int K) {
 // a row-major operand: non-null, 16-byte aligned, rows of at least `width`
 // elements that start at multiples of `mult` elements
 lora_status check_rows(const void* p, int64_t ld, int64_t width, int64_t mult) {
-  if (p == nullptr || ld < width || ld > (int64_t)1 << 40) return LORA_ERR_INVALID_ARG;
+  if (p == nullptr || ld < width) return LORA_ERR_INVALID_ARG;
+  if (ld > (int64_t)1 << 38) return LORA_ERR_UNSUPPORTED;   // a tensor map's stride
   if (!aligned(p, 16) || ld % mult != 0) return LORA_ERR_MISALIGNED;
   return LORA_OK;
 }

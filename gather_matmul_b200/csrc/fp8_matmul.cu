@@ -1,7 +1,25 @@
-// Block-scaled e4m3 matrix product:
+// Block-scaled e4m3 matrix product on tcgen05:
 //   y[t][n] = sum_b q_scale[t][b] w_scale[n/128][b] sum_{k in b} q[t][k] W[n][k]
-// with fp32 products and sums and one rounding.
-#include <cuda_fp8.h>
+//
+// One scale block is 128 columns = one 128-byte swizzled row of a K-major
+// operand tile = four kind::f8f6f4 MMAs of K = 32.  The scales are arbitrary
+// fp32 numbers that change with every block, so no accumulator can live in
+// tensor memory across blocks: each block's product goes to a tensor-memory
+// buffer of its own, and warps beside the pipeline read it and add it, times
+// its scale, to fp32 sums in registers ("promotion") while the tensor core
+// works on the next block in another buffer.
+//
+// Two kernels:
+//   wide    256 tokens x 256 outputs per pair of CTAs (cta_group::2), tokens on
+//           the MMA's M side.  Bound by the tensor core and the promotion.
+//   narrow  128 outputs x 16..128 tokens per CTA, weights on the M side, K split
+//           over a cluster.  Bound by reading the weights once.
+//
+// A wait that runs out (a second; never in a sound run) ends the kernel and
+// makes its outputs NaN.
+#include <string.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -11,88 +29,558 @@ namespace lora {
 
 namespace {
 
-constexpr int kMT = 64, kMN = 64, kMThreads = 256;
+constexpr int kBlockK = LORA_FP8_BLOCK;
 
-__device__ __forceinline__ void e4m3x16(const uint4& v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 p = __half22float2(__half2(h));
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
+__device__ __forceinline__ char* align1024(char* p) {
+  return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// 16 values from column c of a row of K columns, 0 past its end.
-__device__ __forceinline__ uint4 load16(const uint8_t* row, int c, int K) {
-  if (c + 16 <= K) return *reinterpret_cast<const uint4*>(row + c);
-  uint32_t w[4] = {0, 0, 0, 0};
-  for (int i = 0; i < 16; ++i)
-    if (c + i < K) w[i / 4] |= (uint32_t)row[c + i] << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// After a timed-out wait: let copies in flight into this CTA's shared memory
+// land before it exits (10 ms, a bound and not a measure).
+__device__ __forceinline__ void drain_copies() {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (ptx::globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
 }
 
-// 64 x 64 outputs per CTA, 4 x 4 per thread, 32 columns of K at a time.
+// ---------------------------------------------------------------------------
+// Wide: a pair of CTAs per 256 x 256 tile
+// ---------------------------------------------------------------------------
+constexpr int kWTile = 256;                 // tokens and outputs per pair
+constexpr int kWHalf = 128;                 // rows of A and of B that one CTA loads
+constexpr int kWStages = 4;
+constexpr int kWPromote = 8;                // promotion warps
+constexpr int kWThreads = 32 * (kWPromote + 2);
+
+struct WideSmem {
+  static constexpr int kOperand = kWHalf * kBlockK;             // 16 KB
+  static constexpr int kStage = 2 * kOperand;
+  static constexpr int kOut = kWStages * kStage;                // 2 x 4 KB per promotion warp
+  static constexpr int kBar = kOut + kWPromote * 2 * 4096;
+  static constexpr int kTotal = kBar + 8 * (2 * kWStages + 4) + 64 + 1024;
+};
+static_assert(WideSmem::kTotal <= 227 * 1024, "one CTA per SM");
+
+struct WideParams {
+  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128} bytes; y {64, 32} elements
+  const float* q_scale;
+  const float* w_scale;
+  uint16_t* y;
+  int64_t ldy;
+  int T, N, KB, NB, KS;
+  int m_tiles, n_tiles;
+};
+
+// Tile order: groups of 8 token tiles, output tiles within a group, so that the
+// CTAs of one wave share few rows of x and of W.
+__device__ __forceinline__ void wide_tile(const WideParams& P, int tile, int& m0, int& n0) {
+  const int per = 8 * P.n_tiles;
+  const int g = tile / per, r = tile % per;
+  const int gm = min(8, P.m_tiles - 8 * g);
+  m0 = (8 * g + r % gm) * kWTile;
+  n0 = (r / gm) * kWTile;
+}
+
 template <typename E>
-__global__ void __launch_bounds__(kMThreads) matmul_fp8_kernel(MatmulFp8Args a) {
+__global__ void __launch_bounds__(kWThreads, 1)
+matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
+  using L = WideSmem;
+  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWTile);
+  extern __shared__ char smem_raw[];
+  char* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + kWStages;
+  uint64_t* tfull = empty + kWStages;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = ptx::cluster_rank(), half = rank & 1, leader = rank & ~1u;
+  const int KS = P.KS, part = (int)(rank >> 1);
+  const int n_tiles = P.m_tiles * P.n_tiles;
+  const int first = blockIdx.x / (2 * KS), stride = gridDim.x / (2 * KS);
+  const int kb0 = part * P.KB / KS, kb1 = (part + 1) * P.KB / KS;
+
+  if (tid == 0) {
+    for (int s = 0; s < kWStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&tfull[b], 1);
+      ptx::mbar_init(&tempty[b], 2 * kWPromote);
+    }
+    ptx::fence_mbar_init();
+    *stop = 0;
+    ptx::prefetch_tensormap(&P.tmQ);
+    ptx::prefetch_tensormap(&P.tmW);
+    ptx::prefetch_tensormap(&P.tmY);
+  }
+  if (warp == kWPromote + 1) {
+    ptx::tmem_alloc_pair(tmem_slot, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_arrive();
+  ptx::cluster_wait();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
-  __shared__ float sq[32][kMT + 4], sw[32][kMN + 4];
-  const int t0 = blockIdx.x * kMT, n0 = blockIdx.y * kMN;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int KB = (a.K + LORA_FP8_BLOCK - 1) / LORA_FP8_BLOCK;
-  float acc[4][4] = {};
-  for (int b = 0; b < KB; ++b) {
-    float part[4][4] = {};
-    for (int k0 = b * LORA_FP8_BLOCK; k0 < min(a.K, (b + 1) * LORA_FP8_BLOCK); k0 += 32) {
-      __syncthreads();
-      const int r = (threadIdx.x & 127) >> 1, c = (threadIdx.x & 1) * 16;
-      const bool left = threadIdx.x < 128;
-      const bool in = left ? t0 + r < a.T : n0 + r < a.N;
-      float f[16] = {};
-      if (in && k0 + c < a.K)
-        e4m3x16(left ? load16(static_cast<const uint8_t*>(a.q) + (t0 + r) * a.ldq, k0 + c, a.K)
-                     : load16(static_cast<const uint8_t*>(a.W) + (n0 + r) * a.ldw, k0 + c, a.K),
-                f);
-      for (int i = 0; i < 16; ++i) (left ? sq[c + i] : sw[c + i])[r] = f[i];
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            part[i][j] = fmaf(sq[k][ty * 4 + i], sw[k][tx * 4 + j], part[i][j]);
+
+  if (warp == kWPromote) {
+    if (lane == 0) {
+      int it = 0;
+      for (int tile = first; tile < n_tiles && !*stop; tile += stride) {
+        int m0, n0;
+        wide_tile(P, tile, m0, n0);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kWStages;
+          if (it >= kWStages && !ptx::mbar_wait_ff(&empty[s], (it / kWStages - 1) & 1, stop)) break;
+          char* st = smem + s * L::kStage;
+          const uint32_t bar = ptx::map_rank(&full[s], leader);
+          if (half == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
+          ptx::tma_load_2d_pair(st, &P.tmQ, kb * kBlockK, m0 + (int)half * kWHalf, bar);
+          ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK, n0 + (int)half * kWHalf, bar);
+        }
+      }
+      // the last stages' release: no signal may arrive after this CTA has left
+      for (int i = max(it - kWStages, 0); i < it; ++i)
+        if (!ptx::mbar_wait_ff(&empty[i % kWStages], (i / kWStages) & 1, stop)) break;
     }
-    const float ws = a.w_scale[(int64_t)(n0 / LORA_FP8_BLOCK) * KB + b];
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + ty * 4 + i;
-      const float s = t < a.T ? a.q_scale[(int64_t)t * KB + b] * ws : 0.f;
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s, part[i][j], acc[i][j]);
+    __syncwarp();
+  } else if (warp == kWPromote + 1) {
+    if (lane == 0 && half == 0) {
+      const uint32_t sbase = ptx::smem_u32(smem);
+      const uint16_t mask = (uint16_t)(3u << leader);
+      const int total = ((n_tiles - first + stride - 1) / stride) * (kb1 - kb0);
+      for (int it = 0; it < total; ++it) {
+        const int s = it % kWStages, b = it & 1;
+        if (it >= 2 && !ptx::mbar_wait_ff(&tempty[b], (it / 2 - 1) & 1, stop)) break;
+        if (!ptx::mbar_wait_ff(&full[s], (it / kWStages) & 1, stop)) break;
+        ptx::tc_fence_after();
+        const uint32_t qa = sbase + s * L::kStage, wa = qa + L::kOperand;
+#pragma unroll
+        for (int k = 0; k < kBlockK / 32; ++k)
+          ptx::tc_mma_f8_pair(tmem + b * kWTile, ptx::umma_desc_kmajor(qa + k * 32, 128),
+                              ptx::umma_desc_kmajor(wa + k * 32, 128), kIdesc, k > 0);
+        ptx::tc_commit_pair(&empty[s], mask);
+        ptx::tc_commit_pair(&tfull[b], mask);
+      }
+    }
+    __syncwarp();
+  } else {
+    // promotion: thread = token row, one half of the columns per four warps
+    const int row = (warp & 3) * 32 + lane, ch = warp >> 2;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + ch * kWHalf;
+    const uint32_t te0 = ptx::map_rank(&tempty[0], leader), te1 = ptx::map_rank(&tempty[1], leader);
+    char* out = smem + L::kOut + warp * 2 * 4096;
+    int it = 0;
+    for (int tile = first; tile < n_tiles; tile += stride) {
+      int m0, n0;
+      wide_tile(P, tile, m0, n0);
+      m0 += (int)half * kWHalf;
+      n0 += ch * kWHalf;
+      const int t = m0 + row;
+      const float* qs = P.q_scale + (int64_t)min(t, P.T - 1) * P.KB;
+      const float* ws = P.w_scale + (int64_t)min(n0 / kBlockK, P.NB - 1) * P.KB;
+      uint64_t acc[kWHalf / 2];
+#pragma unroll
+      for (int i = 0; i < kWHalf / 2; ++i) acc[i] = 0;
+      float sq = qs[kb0], sw = ws[kb0];
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const float s = sq * sw;
+        const uint64_t s2 = ptx::pack2(s, s);
+        if (kb + 1 < kb1) {
+          sq = qs[kb + 1];
+          sw = ws[kb + 1];
+        }
+        const int b = it & 1;
+        ok = ok && ptx::mbar_wait_ff(&tfull[b], (it / 2) & 1, stop);
+        __syncwarp();
+        ptx::tc_fence_after();
+        uint32_t r[2][16];
+        ptx::tc_ld16(trow + b * kWTile, r[0]);
+#pragma unroll
+        for (int c = 0; c < kWHalf / 16; ++c) {
+          ptx::tc_wait_ld();
+          if (c + 1 < kWHalf / 16) ptx::tc_ld16(trow + b * kWTile + (c + 1) * 16, r[(c + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t v = (uint64_t)r[c & 1][2 * i] | ((uint64_t)r[c & 1][2 * i + 1] << 32);
+            acc[c * 8 + i] = ptx::ffma2(s2, v, acc[c * 8 + i]);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(b ? te1 : te0);
+      }
+      if (!ok) {
+#pragma unroll
+        for (int i = 0; i < kWHalf / 2; ++i) acc[i] = 0x7fffffff7fffffffull;
+      }
+      if (KS == 1) {
+        // 32 rows x 64 columns at a time through shared memory, in the 128-byte
+        // swizzle the tensor map expects, and out by TMA.  TMA clips at T, but in
+        // a row only at whole 16 bytes: the map ends at N rounded down to 8, and
+        // the last columns are stored one by one
+        const int n8 = P.N & ~7;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 0) {
+            if (lane == 0) ptx::bulk_wait_read_all();   // the previous tile's copies have left
+            __syncwarp();
+          }
+          char* o = out + h * 4096 + lane * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 v;
+            uint32_t* w = &v.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t a = acc[h * 32 + j * 4 + i];
+              w[i] = Elem<E>::pack2(ptx::lo32(a), ptx::hi32(a));
+            }
+            *reinterpret_cast<uint4*>(o + ((j ^ (lane & 7)) << 4)) = v;
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          const int mr = m0 + (warp & 3) * 32, nc = n0 + h * 64;
+          if (lane == 0) {
+            if (mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, out + h * 4096);
+            ptx::bulk_commit();
+          }
+          if (n8 >= nc && n8 < nc + 64 && t < P.T) {
+            const uint16_t* v =
+                reinterpret_cast<const uint16_t*>(o + ((((n8 - nc) >> 3) ^ (lane & 7)) << 4));
+            for (int n = n8; n < P.N; ++n) P.y[(int64_t)t * P.ldy + n] = v[n - n8];
+          }
+        }
+      } else {
+        // one tile per cluster: part p of K hands each other part its share of the
+        // columns (128 / KS of this thread's), through the drained stages
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+        const int share = kWHalf / KS, me = warp * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < kWHalf; ++i) {
+          const uint32_t dst = ptx::map_rank(smem, (uint32_t)(i / share) * 2 + half);
+          const uint64_t a = acc[i / 2];
+          ptx::st_cluster_f32(dst + 4 * ((part * share + i % share) * 32 * kWPromote + me),
+                              i & 1 ? ptx::hi32(a) : ptx::lo32(a));
+        }
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+        const float* recv = reinterpret_cast<const float*>(smem);
+        for (int i = 0; i < share; ++i) {
+          float v = 0.f;
+          for (int p = 0; p < KS; ++p) v += recv[(p * share + i) * 32 * kWPromote + me];
+          const int n = n0 + part * share + i;
+          if (t < P.T && n < P.N) P.y[(int64_t)t * P.ldy + n] = Elem<E>::from_f32(v);
+        }
+      }
+    }
+    if (lane == 0) ptx::bulk_wait_all();
+    __syncwarp();
+  }
+  if (KS > 1 && warp >= kWPromote) {
+    // the promotion warps' two cluster barriers
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+  }
+  if (*stop && tid == 0) drain_copies();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_arrive();     // no CTA leaves while a peer may still signal it
+  ptx::cluster_wait();
+  if (warp == kWPromote + 1) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Narrow: 128 outputs x TN tokens per CTA, K split over a cluster
+// ---------------------------------------------------------------------------
+constexpr int kNRows = 128;
+constexpr int kNThreads = 192;      // warps 0-3 promotion, 4 copies, 5 MMA
+
+template <int TN>
+struct NarrowSmem {
+  static constexpr int kW = kNRows * kBlockK;
+  static constexpr int kStage = kW + TN * kBlockK;
+  static constexpr int kStages = TN == 128 ? 3 : (TN == 64 ? 4 : 5);   // two CTAs per SM
+  static constexpr int kBufs = TN == 128 ? 2 : 4;                      // tensor-memory buffers
+  static constexpr int kCols = TN * kBufs;
+  static constexpr int kScale = kStages * kStage;                      // 2 x TN floats
+  static constexpr int kBar = kScale + 2 * TN * 4;
+  static constexpr int kTotal = kBar + 8 * (2 * kStages + 2 * kBufs) + 64 + 1024;
+};
+
+struct NarrowParams {
+  CUtensorMap tmQ, tmW;     // boxes {128, TN}, {128, 128} bytes
+  const float* q_scale;
+  const float* w_scale;
+  uint16_t* y;
+  int64_t ldy;
+  int T, N, KB, KS, n_tiles;
+};
+
+template <typename E, int TN>
+__global__ void __launch_bounds__(kNThreads, 2)
+matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
+  using L = NarrowSmem<TN>;
+  constexpr int kS = L::kStages, kB = L::kBufs;
+  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kNRows, TN);
+  extern __shared__ char smem_raw[];
+  char* smem = align1024(smem_raw);
+  float* scale = reinterpret_cast<float*>(smem + L::kScale);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + kS;
+  uint64_t* tfull = empty + kS;
+  uint64_t* tempty = tfull + kB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + kB);
+  volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int KS = P.KS, part = (int)ptx::cluster_rank();
+  const int unit = blockIdx.x / KS;
+  const int n0 = (unit % P.n_tiles) * kNRows, t0 = (unit / P.n_tiles) * TN;
+  const int kb0 = part * P.KB / KS, nkb = (part + 1) * P.KB / KS - kb0;
+
+  if (tid == 0) {
+    for (int s = 0; s < kS; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kB; ++b) {
+      ptx::mbar_init(&tfull[b], 1);
+      ptx::mbar_init(&tempty[b], 4);
+    }
+    ptx::fence_mbar_init();
+    *stop = 0;
+    ptx::prefetch_tensormap(&P.tmQ);
+    ptx::prefetch_tensormap(&P.tmW);
+  }
+  if (warp == 5) {
+    ptx::tmem_alloc(tmem_slot, L::kCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch_dependents();
+
+  float acc[TN];
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % kS;
+        if (i >= kS && !ptx::mbar_wait_ff(&empty[s], (i / kS - 1) & 1, stop)) break;
+        char* st = smem + s * L::kStage;
+        ptx::mbar_arrive_expect_tx(&full[s], L::kStage);
+        ptx::tma_load_2d(st, &P.tmW, (kb0 + i) * kBlockK, n0, &full[s]);
+        ptx::tma_load_2d(st + L::kW, &P.tmQ, (kb0 + i) * kBlockK, t0, &full[s]);
+      }
+      // the last stages' release: no signal may arrive after this CTA has left
+      for (int i = max(nkb - kS, 0); i < nkb; ++i)
+        if (!ptx::mbar_wait_ff(&empty[i % kS], (i / kS) & 1, stop)) break;
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t sbase = ptx::smem_u32(smem);
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % kS, b = i % kB;
+        if (i >= kB && !ptx::mbar_wait_ff(&tempty[b], (i / kB - 1) & 1, stop)) break;
+        if (!ptx::mbar_wait_ff(&full[s], (i / kS) & 1, stop)) break;
+        ptx::tc_fence_after();
+        const uint32_t wa = sbase + s * L::kStage, qa = wa + L::kW;
+#pragma unroll
+        for (int k = 0; k < kBlockK / 32; ++k)
+          ptx::tc_mma_f8(tmem + b * TN, ptx::umma_desc_kmajor(wa + k * 32, 128),
+                         ptx::umma_desc_kmajor(qa + k * 32, 128), kIdesc, k > 0);
+        ptx::tc_commit(&empty[s]);
+        ptx::tc_commit(&tfull[b]);
+      }
+    }
+    __syncwarp();
+  } else {
+    // promotion: thread = output row, columns = tokens; the tokens' scales of a
+    // block, times the tile's one weight scale, go through shared memory
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    const float* ws = P.w_scale + (int64_t)(n0 / kBlockK) * P.KB + kb0;
+    const float* qs = P.q_scale + (int64_t)min(t0 + tid, P.T - 1) * P.KB + kb0;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[j] = 0.f;
+    bool ok = true;
+    float next = tid < TN ? qs[0] * ws[0] : 0.f;
+    for (int i = 0; i < nkb; ++i) {
+      float* sc = scale + (i & 1) * TN;
+      if (tid < TN) sc[tid] = next;
+      if (i + 1 < nkb && tid < TN) next = qs[i + 1] * ws[i + 1];
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const int b = i % kB;
+      ok = ok && ptx::mbar_wait_ff(&tfull[b], (i / kB) & 1, stop);
+      __syncwarp();
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < TN / 16; ++c) {
+        uint32_t r[16];
+        ptx::tc_ld16(trow + b * TN + c * 16, r);
+        ptx::tc_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          acc[c * 16 + j] = fmaf(sc[c * 16 + j], __uint_as_float(r[j]), acc[c * 16 + j]);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&tempty[b]);
+    }
+    if (!ok) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[j] = __int_as_float(0x7fffffff);
     }
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = t0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (t < a.T && n < a.N)
-        static_cast<uint16_t*>(a.y)[t * a.ldy + n] = Elem<E>::from_f32(acc[i][j]);
+  const int n = n0 + tid;
+  if (KS == 1) {
+    if (warp < 4 && n < P.N) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        if (t0 + j < P.T) P.y[(int64_t)(t0 + j) * P.ldy + n] = Elem<E>::from_f32(acc[j]);
     }
+  } else {
+    // part p of K hands every other part its share of the tokens (TN / KS),
+    // through the drained stages; each adds the KS shares in rank order
+    const int share = TN / KS;
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    if (warp < 4) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        ptx::st_cluster_f32(ptx::map_rank(smem, (uint32_t)(j / share)) +
+                                4 * ((part * share + j % share) * kNRows + tid),
+                            acc[j]);
+    }
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    const float* recv = reinterpret_cast<const float*>(smem);
+    if (warp < 4 && n < P.N) {
+      for (int j = 0; j < share; ++j) {
+        const int t = t0 + part * share + j;
+        if (t >= P.T) break;
+        float v = 0.f;
+        for (int p = 0; p < KS; ++p) v += recv[(p * share + j) * kNRows + tid];
+        P.y[(int64_t)t * P.ldy + n] = Elem<E>::from_f32(v);
+      }
+    }
+  }
+  if (*stop && tid == 0) drain_copies();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 5) ptx::tmem_dealloc(tmem, L::kCols);
+}
+
+int sm_count() {
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (cache[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      n = 148;
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <typename Kern, typename Params>
+cudaError_t cluster_launch(Kern kern, const Params& P, unsigned grid, unsigned cluster,
+                           unsigned threads, size_t smem, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return counted_launch(cudaLaunchKernelEx(&cfg, kern, P));
+}
+
+template <typename E>
+cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) {
+  WideParams P;
+  memset(&P, 0, sizeof(P));
+  cudaError_t e = encode_tmap_2d_bytes(&P.tmQ, a.q, a.K, a.T, a.ldq, kBlockK, kWHalf, 128);
+  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, kWHalf, 128);
+  if (e == cudaSuccess) e = encode_tmap_2d(&P.tmY, dt, a.y, a.N < 8 ? 8 : a.N & ~7, a.T,
+                                           (uint64_t)a.ldy * 2, 64, 32, 128);
+  if (e != cudaSuccess) return e;
+  P.q_scale = a.q_scale;
+  P.w_scale = a.w_scale;
+  P.y = static_cast<uint16_t*>(a.y);
+  P.ldy = a.ldy;
+  P.T = a.T;
+  P.N = a.N;
+  P.KB = (a.K + kBlockK - 1) / kBlockK;
+  P.NB = (a.N + kBlockK - 1) / kBlockK;
+  P.m_tiles = (a.T + kWTile - 1) / kWTile;
+  P.n_tiles = (a.N + kWTile - 1) / kWTile;
+  const int tiles = P.m_tiles * P.n_tiles, pairs = sm_count() / 2;
+  int KS = 1;
+  while (KS < 4 && tiles * KS * 2 <= pairs && P.KB >= 4 * KS) KS *= 2;
+  P.KS = KS;
+  const int clusters = KS > 1 ? tiles : (tiles < pairs ? tiles : pairs);
+  return cluster_launch(matmul_fp8_wide_kernel<E>, P, clusters * 2 * KS, 2 * KS, kWThreads,
+                        WideSmem::kTotal, st);
+}
+
+template <typename E, int TN>
+cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
+  NarrowParams P;
+  memset(&P, 0, sizeof(P));
+  cudaError_t e = encode_tmap_2d_bytes(&P.tmQ, a.q, a.K, a.T, a.ldq, kBlockK, TN, 128);
+  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, kNRows, 128);
+  if (e != cudaSuccess) return e;
+  P.q_scale = a.q_scale;
+  P.w_scale = a.w_scale;
+  P.y = static_cast<uint16_t*>(a.y);
+  P.ldy = a.ldy;
+  P.T = a.T;
+  P.N = a.N;
+  P.KB = (a.K + kBlockK - 1) / kBlockK;
+  P.n_tiles = (a.N + kNRows - 1) / kNRows;
+  const int units = P.n_tiles * ((a.T + TN - 1) / TN);
+  int KS = 1;
+  while (KS < 8 && units * KS * 2 <= 2 * sm_count() && P.KB >= 4 * KS) KS *= 2;
+  P.KS = KS;
+  return cluster_launch(matmul_fp8_narrow_kernel<E, TN>, P, units * KS, KS, kNThreads,
+                        NarrowSmem<TN>::kTotal, st);
+}
+
+template <typename E>
+cudaError_t matmul_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) {
+  if (a.T <= 16) return narrow_launch<E, 16>(a, st);
+  if (a.T <= 32) return narrow_launch<E, 32>(a, st);
+  if (a.T <= 64) return narrow_launch<E, 64>(a, st);
+  if (a.T <= 128) return narrow_launch<E, 128>(a, st);
+  return wide_launch<E>(dt, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_matmul_fp8(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kMThreads, 1, 1);
-  cfg.gridDim = dim3((a.T + kMT - 1) / kMT, (a.N + kMN - 1) / kMN, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return counted_launch(dt == LORA_BF16
-                            ? cudaLaunchKernelEx(&cfg, matmul_fp8_kernel<__nv_bfloat16>, a)
-                            : cudaLaunchKernelEx(&cfg, matmul_fp8_kernel<__half>, a));
+  return dt == LORA_BF16 ? matmul_launch<__nv_bfloat16>(dt, a, st)
+                         : matmul_launch<__half>(dt, a, st);
 }
 
 }  // namespace lora

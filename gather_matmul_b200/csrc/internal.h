@@ -122,6 +122,11 @@ cudaError_t encode_tmap_2d(CUtensorMap* map, lora_dtype dt, const void* base, ui
                            uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                            uint32_t box_outer, int swizzle_bytes);
 
+// the same for 8-bit elements
+cudaError_t encode_tmap_2d_bytes(CUtensorMap* map, const void* base, uint64_t inner,
+                                 uint64_t outer, uint64_t row_stride, uint32_t box_inner,
+                                 uint32_t box_outer, int swizzle_bytes);
+
 // Whether the fused kernel takes this shape (host-side, no CUDA calls).
 bool bgmv_fused_fits(int T, int D, int r, int n_slices, const int32_t* D_out);
 // Returns cudaErrorNotSupported when the shape does not fit the fused kernel.

@@ -27,9 +27,9 @@ EncodeTiledFn encode_fn() {
 }
 }  // namespace
 
-cudaError_t encode_tmap_2d(CUtensorMap* map, lora_dtype dt, const void* base, uint64_t inner,
-                           uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
-                           uint32_t box_outer, int swizzle_bytes) {
+static cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                          uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
+                          uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
   cuuint64_t dims[2] = {inner, outer};
@@ -40,13 +40,26 @@ cudaError_t encode_tmap_2d(CUtensorMap* map, lora_dtype dt, const void* base, ui
                           : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                           : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = fn(map,
-                  dt == LORA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  2, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_tmap_2d(CUtensorMap* map, lora_dtype dt, const void* base, uint64_t inner,
+                           uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
+                           uint32_t box_outer, int swizzle_bytes) {
+  return encode(map,
+                dt == LORA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                base, inner, outer, row_stride_bytes, box_inner, box_outer, swizzle_bytes);
+}
+
+cudaError_t encode_tmap_2d_bytes(CUtensorMap* map, const void* base, uint64_t inner,
+                                 uint64_t outer, uint64_t row_stride, uint32_t box_inner,
+                                 uint32_t box_outer, int swizzle_bytes) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, row_stride, box_inner,
+                box_outer, swizzle_bytes);
 }
 
 }  // namespace lora
