@@ -21,6 +21,10 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-cudart", "static"]
 
+# Compiled as whole programs: under relocatable device code ptxas ignores
+# setmaxnreg, and no device symbol of these files is used by another.
+WHOLE = {"fp8_matmul.cu", "fp8_quant.cu", "rope.cu"}
+
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -46,7 +50,8 @@ def build(force=False, verbose=False, out=LIB, extra=()):
     objs = []
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
-        cmd = [NVCC, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-dc", "-o", obj, src]
+        cmd = [NVCC, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC,
+               "-c" if os.path.basename(src) in WHOLE else "-dc", "-o", obj, src]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd))

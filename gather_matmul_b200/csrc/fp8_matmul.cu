@@ -48,20 +48,26 @@ __device__ __forceinline__ void drain_copies() {
 constexpr int kWTile = 256;                 // tokens and outputs per pair
 constexpr int kWHalf = 128;                 // rows of A and of B that one CTA loads
 constexpr int kWStages = 4;
+constexpr int kWBufs = 4;                   // tensor-memory buffers of 128 columns
 constexpr int kWPromote = 8;                // promotion warps
-constexpr int kWThreads = 32 * (kWPromote + 2);
+constexpr int kWSlots = 4;                  // groups of 4 blocks whose scales are in shared memory
+constexpr int kWThreads = 32 * (kWPromote + 4);
+// registers: 168 a thread at launch (384 threads); 2 x 232 + 40 = 3 x 168
+constexpr int kWRegsPromote = 232, kWRegsRest = 40;
 
 struct WideSmem {
   static constexpr int kOperand = kWHalf * kBlockK;             // 16 KB
   static constexpr int kStage = 2 * kOperand;
   static constexpr int kOut = kWStages * kStage;                // 2 x 4 KB per promotion warp
-  static constexpr int kBar = kOut + kWPromote * 2 * 4096;
-  static constexpr int kTotal = kBar + 8 * (2 * kWStages + 4) + 64 + 1024;
+  static constexpr int kScale = kOut + kWPromote * 8192;        // per slot: 4 of 128 tokens, 4 of 2 of W
+  static constexpr int kSlot = 16 * (kWHalf + 2);
+  static constexpr int kBar = kScale + kWSlots * kSlot;
+  static constexpr int kTotal = kBar + 8 * 2 * (kWStages + kWBufs + kWSlots) + 64 + 1024;
 };
 static_assert(WideSmem::kTotal <= 227 * 1024, "one CTA per SM");
 
 struct WideParams {
-  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128} bytes; y {64, 32} elements
+  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128}, {128, 64} bytes; y {64, 32} elements
   const float* q_scale;
   const float* w_scale;
   uint16_t* y;
@@ -84,16 +90,20 @@ template <typename E>
 __global__ void __launch_bounds__(kWThreads, 1)
 matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   using L = WideSmem;
-  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWTile);
+  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWHalf);
   extern __shared__ char smem_raw[];
   char* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* empty = full + kWStages;
   uint64_t* tfull = empty + kWStages;
-  uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* tempty = tfull + kWBufs;
+  uint64_t* sfull = tempty + kWBufs;
+  uint64_t* sempty = sfull + kWSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kWSlots);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t stop_at = ptx::smem_u32(tmem_slot + 1);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);     // uniform in the warp
   const uint32_t rank = ptx::cluster_rank(), half = rank & 1, leader = rank & ~1u;
   const int KS = P.KS, part = (int)(rank >> 1);
   const int n_tiles = P.m_tiles * P.n_tiles;
@@ -103,11 +113,15 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   if (tid == 0) {
     for (int s = 0; s < kWStages; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
+      ptx::mbar_init(&empty[s], 2);             // both issuing warps
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kWBufs; ++b) {
       ptx::mbar_init(&tfull[b], 1);
       ptx::mbar_init(&tempty[b], 2 * kWPromote);
+    }
+    for (int s = 0; s < kWSlots; ++s) {
+      ptx::mbar_init(&sfull[s], 32);
+      ptx::mbar_init(&sempty[s], kWPromote);
     }
     ptx::fence_mbar_init();
     *stop = 0;
@@ -128,156 +142,247 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
 
-  if (warp == kWPromote) {
-    if (lane == 0) {
-      int it = 0;
+  if (warp >= kWPromote) {
+    ptx::reg_dec<kWRegsRest>();
+    if (warp == kWPromote) {
+      // operand tiles of this CTA's half
+      if (lane == 0) {
+        int it = 0;
+        const uint32_t bar0 = ptx::map_rank(full, leader), em = ptx::smem_u32(empty);
+        for (int tile = first; tile < n_tiles && !*stop; tile += stride) {
+          int m0, n0;
+          wide_tile(P, tile, m0, n0);
+          for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const int s = it % kWStages;
+            if (it >= kWStages && !ptx::mbar_wait_asm(em + 8 * s, (it / kWStages - 1) & 1, stop_at))
+              break;
+            char* st = smem + s * L::kStage;
+            const uint32_t bar = bar0 + 8 * s;
+            if (half == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
+            ptx::tma_load_2d_pair(st, &P.tmQ, kb * kBlockK, m0 + (int)half * kWHalf, bar);
+            // W's rows in two boxes of 64: the MMA of output half h takes rows
+            // h * 64 .. of either CTA, which then are h * 128 + half * 64 .. of the tile
+            ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK, n0 + (int)half * 64, bar);
+            ptx::tma_load_2d_pair(st + L::kOperand + 64 * kBlockK, &P.tmW, kb * kBlockK,
+                                  n0 + kWHalf + (int)half * 64, bar);
+          }
+        }
+        // the last stages' release: no signal may arrive after this CTA has left
+        for (int i = max(it - kWStages, 0); i < it; ++i)
+          if (!ptx::mbar_wait_asm(em + 8 * (i % kWStages), (i / kWStages) & 1, stop_at)) break;
+      }
+    } else if (warp == kWPromote + 2) {
+      // scales, in groups of 4 blocks: 128 of this CTA's tokens and two of W
+      const bool wide16 = P.KB % 4 == 0 && kb0 % 4 == 0 &&
+                          ((reinterpret_cast<uintptr_t>(P.q_scale) |
+                            reinterpret_cast<uintptr_t>(P.w_scale)) & 15) == 0;
+      const uint32_t sf = ptx::smem_u32(sfull), se = ptx::smem_u32(sempty);
+      int g = 0;
       for (int tile = first; tile < n_tiles && !*stop; tile += stride) {
         int m0, n0;
         wide_tile(P, tile, m0, n0);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kWStages;
-          if (it >= kWStages && !ptx::mbar_wait_ff(&empty[s], (it / kWStages - 1) & 1, stop)) break;
-          char* st = smem + s * L::kStage;
-          const uint32_t bar = ptx::map_rank(&full[s], leader);
-          if (half == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
-          ptx::tma_load_2d_pair(st, &P.tmQ, kb * kBlockK, m0 + (int)half * kWHalf, bar);
-          ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK, n0 + (int)half * kWHalf, bar);
+        m0 += (int)half * kWHalf;
+        const float* src[5];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          src[i] = P.q_scale + (int64_t)min(m0 + i * 32 + lane, P.T - 1) * P.KB;
+        src[4] = P.w_scale + (int64_t)min(n0 / kBlockK + (lane & 1), P.NB - 1) * P.KB;
+        for (int kb = kb0; kb < kb1; kb += 4, ++g) {
+          const int s = g % kWSlots;
+          if (g >= kWSlots && !ptx::mbar_wait_asm(se + 8 * s, (g / kWSlots - 1) & 1, stop_at)) break;
+          float* dst = reinterpret_cast<float*>(smem + L::kScale + s * L::kSlot);
+          const int n = min(4, kb1 - kb);
+          if (wide16 && n == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ptx::cp_async16(dst + 4 * (i * 32 + lane), src[i] + kb);
+            if (lane < 2) ptx::cp_async16(dst + 4 * (kWHalf + lane), src[4] + kb);
+          } else {
+            for (int j = 0; j < n; ++j) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                ptx::cp_async4(dst + 4 * (i * 32 + lane) + j, src[i] + kb + j);
+              if (lane < 2) ptx::cp_async4(dst + 4 * (kWHalf + lane) + j, src[4] + kb + j);
+            }
+          }
+          ptx::cp_async_arrive(&sfull[s]);
         }
       }
-      // the last stages' release: no signal may arrive after this CTA has left
-      for (int i = max(it - kWStages, 0); i < it; ++i)
-        if (!ptx::mbar_wait_ff(&empty[i % kWStages], (i / kWStages) & 1, stop)) break;
-    }
-    __syncwarp();
-  } else if (warp == kWPromote + 1) {
-    if (lane == 0 && half == 0) {
-      const uint32_t sbase = ptx::smem_u32(smem);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (half == 0) {
+      // one issuing warp per output half, in the pair's even CTA: the whole warp
+      // runs the loop, an elected thread issues
+      const int h = warp == kWPromote + 1 ? 0 : 1;
+      const bool one = ptx::elect_one();
+      const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty + h);
+      const uint64_t dq = ptx::umma_desc_kmajor(ptx::smem_u32(smem), 128);
+      const uint64_t dw =
+          ptx::umma_desc_kmajor(ptx::smem_u32(smem) + L::kOperand + h * 64 * kBlockK, 128);
       const uint16_t mask = (uint16_t)(3u << leader);
       const int total = ((n_tiles - first + stride - 1) / stride) * (kb1 - kb0);
       for (int it = 0; it < total; ++it) {
         const int s = it % kWStages, b = it & 1;
-        if (it >= 2 && !ptx::mbar_wait_ff(&tempty[b], (it / 2 - 1) & 1, stop)) break;
-        if (!ptx::mbar_wait_ff(&full[s], (it / kWStages) & 1, stop)) break;
+        bool ok = ptx::mbar_wait_asm(fu + 8 * s, (it / kWStages) & 1, stop_at);
+        if (it >= 2) ok &= ptx::mbar_wait_asm(te + 16 * b, (it / 2 - 1) & 1, stop_at);
+        if (!__all_sync(~0u, ok)) break;
         ptx::tc_fence_after();
-        const uint32_t qa = sbase + s * L::kStage, wa = qa + L::kOperand;
+        if (one) {
+          const uint32_t d = tmem + (2 * b + h) * kWHalf;
+          const uint64_t qa = dq + (uint32_t)(s * (L::kStage >> 4));
+          const uint64_t wa = dw + (uint32_t)(s * (L::kStage >> 4));
 #pragma unroll
-        for (int k = 0; k < kBlockK / 32; ++k)
-          ptx::tc_mma_f8_pair(tmem + b * kWTile, ptx::umma_desc_kmajor(qa + k * 32, 128),
-                              ptx::umma_desc_kmajor(wa + k * 32, 128), kIdesc, k > 0);
-        ptx::tc_commit_pair(&empty[s], mask);
-        ptx::tc_commit_pair(&tfull[b], mask);
+          for (int k = 0; k < kBlockK / 32; ++k)
+            ptx::tc_mma_f8_pair(d, qa + k * 2, wa + k * 2, kIdesc, k > 0);
+          ptx::tc_commit_pair(&tfull[2 * b + h], mask);
+          ptx::tc_commit_pair(&empty[s], mask);
+        }
+        __syncwarp();
       }
     }
     __syncwarp();
   } else {
-    // promotion: thread = token row, one half of the columns per four warps
-    const int row = (warp & 3) * 32 + lane, ch = warp >> 2;
-    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + ch * kWHalf;
-    const uint32_t te0 = ptx::map_rank(&tempty[0], leader), te1 = ptx::map_rank(&tempty[1], leader);
-    char* out = smem + L::kOut + warp * 2 * 4096;
-    int it = 0;
+    ptx::reg_inc<kWRegsPromote>();
+    // promotion: thread = token row; columns 64 * (warp / 4) .. + 63 of either
+    // 128-column half of the tile
+    const int quad = warp & 3, col = (warp >> 2) * 64, row = quad * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col;
+    const uint32_t te = ptx::map_rank(&tempty[0], leader);
+    const uint32_t tf = ptx::smem_u32(tfull), sf = ptx::smem_u32(sfull);
+    char* out = smem + L::kOut + warp * 8192;
+    int it = 0, g = 0;
     for (int tile = first; tile < n_tiles; tile += stride) {
       int m0, n0;
       wide_tile(P, tile, m0, n0);
       m0 += (int)half * kWHalf;
-      n0 += ch * kWHalf;
       const int t = m0 + row;
-      const float* qs = P.q_scale + (int64_t)min(t, P.T - 1) * P.KB;
-      const float* ws = P.w_scale + (int64_t)min(n0 / kBlockK, P.NB - 1) * P.KB;
-      uint64_t acc[kWHalf / 2];
+      uint64_t acc[2][32];
 #pragma unroll
-      for (int i = 0; i < kWHalf / 2; ++i) acc[i] = 0;
-      float sq = qs[kb0], sw = ws[kb0];
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const float s = sq * sw;
-        const uint64_t s2 = ptx::pack2(s, s);
-        if (kb + 1 < kb1) {
-          sq = qs[kb + 1];
-          sw = ws[kb + 1];
-        }
-        const int b = it & 1;
-        ok = ok && ptx::mbar_wait_ff(&tfull[b], (it / 2) & 1, stop);
+      for (int i = 0; i < 64; ++i) acc[i / 32][i % 32] = 0;
+      // 32 columns at a time: the next ones are on their way from tensor memory
+      // while the sums of these are formed
+      uint32_t r0[32], r1[32];
+      bool ok = ptx::mbar_wait_asm(tf + 16 * (it & 1), (it / 2) & 1, stop_at);
+      __syncwarp();
+      ptx::tc_fence_after();
+      ptx::tc_ld32(trow + (it & 1) * 2 * kWHalf, r0);
+      for (int kb = kb0; kb < kb1; kb += 4, ++g) {
+        const int sl = g % kWSlots, n = min(4, kb1 - kb);
+        ok &= ptx::mbar_wait_asm(sf + 8 * sl, (g / kWSlots) & 1, stop_at);
+        const float4* sc = reinterpret_cast<const float4*>(smem + L::kScale + sl * L::kSlot);
+        float4 q4 = sc[row];
+        float4 a4 = sc[kWHalf], b4 = sc[kWHalf + 1];
         __syncwarp();
-        ptx::tc_fence_after();
-        uint32_t r[2][16];
-        ptx::tc_ld16(trow + b * kWTile, r[0]);
-#pragma unroll
-        for (int c = 0; c < kWHalf / 16; ++c) {
-          ptx::tc_wait_ld();
-          if (c + 1 < kWHalf / 16) ptx::tc_ld16(trow + b * kWTile + (c + 1) * 16, r[(c + 1) & 1]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t v = (uint64_t)r[c & 1][2 * i] | ((uint64_t)r[c & 1][2 * i + 1] << 32);
-            acc[c * 8 + i] = ptx::ffma2(s2, v, acc[c * 8 + i]);
+        if (lane == 0) ptx::mbar_arrive(&sempty[sl]);
+        for (int j = 0; j < n; ++j, ++it) {
+          const int b = it & 1;
+          const uint32_t t0 = trow + b * 2 * kWHalf, tn = trow + (b ^ 1) * 2 * kWHalf;
+          const uint32_t ph = (it / 2) & 1, pn = ((it + 1) / 2) & 1;
+          const float s0 = q4.x * a4.x, s1 = q4.x * b4.x;
+          const uint64_t sa = ptx::pack2(s0, s0), sb = ptx::pack2(s1, s1);
+          q4.x = q4.y; q4.y = q4.z; q4.z = q4.w;
+          a4.x = a4.y; a4.y = a4.z; a4.z = a4.w;
+          b4.x = b4.y; b4.y = b4.z; b4.z = b4.w;
+          const bool more = kb + j + 1 < kb1;
+          // half 0, first 32 columns
+          ptx::tc_wait_ld32(r0);
+          ptx::tc_ld32(t0 + 32, r1);
+          ptx::ffma2_acc16(acc[0], sa, r0);
+          // half 0, last 32 columns
+          ptx::tc_wait_ld32(r1);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(te + 16 * b);
+          ok &= ptx::mbar_wait_asm(tf + 16 * b + 8, ph, stop_at);
+          __syncwarp();
+          ptx::tc_fence_after();
+          ptx::tc_ld32(t0 + kWHalf, r0);
+          ptx::ffma2_acc16(acc[0] + 16, sa, r1);
+          // half 1, first 32 columns
+          ptx::tc_wait_ld32(r0);
+          ptx::tc_ld32(t0 + kWHalf + 32, r1);
+          ptx::ffma2_acc16(acc[1], sb, r0);
+          // half 1, last 32 columns; the next block's first
+          ptx::tc_wait_ld32(r1);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(te + 16 * b + 8);
+          if (more) {
+            ok &= ptx::mbar_wait_asm(tf + 16 * (b ^ 1), pn, stop_at);
+            __syncwarp();
+            ptx::tc_fence_after();
+            ptx::tc_ld32(tn, r0);
           }
+          ptx::ffma2_acc16(acc[1] + 16, sb, r1);
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(b ? te1 : te0);
       }
       if (!ok) {
 #pragma unroll
-        for (int i = 0; i < kWHalf / 2; ++i) acc[i] = 0x7fffffff7fffffffull;
+        for (int i = 0; i < 64; ++i) acc[i / 32][i % 32] = 0x7fffffff7fffffffull;
       }
       if (KS == 1) {
-        // 32 rows x 64 columns at a time through shared memory, in the 128-byte
+        // 32 rows x 64 columns per half through shared memory, in the 128-byte
         // swizzle the tensor map expects, and out by TMA.  TMA clips at T, but in
         // a row only at whole 16 bytes: the map ends at N rounded down to 8, and
         // the last columns are stored one by one
         const int n8 = P.N & ~7;
+        if (lane == 0) ptx::bulk_wait_read_all();     // the previous tile's copies have left
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == 0) {
-            if (lane == 0) ptx::bulk_wait_read_all();   // the previous tile's copies have left
-            __syncwarp();
-          }
           char* o = out + h * 4096 + lane * 128;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint4 v;
             uint32_t* w = &v.x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint64_t a = acc[h * 32 + j * 4 + i];
-              w[i] = Elem<E>::pack2(ptx::lo32(a), ptx::hi32(a));
-            }
+            for (int i = 0; i < 4; ++i)
+              w[i] = Elem<E>::pack2(ptx::lo32(acc[h][j * 4 + i]), ptx::hi32(acc[h][j * 4 + i]));
             *reinterpret_cast<uint4*>(o + ((j ^ (lane & 7)) << 4)) = v;
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          const int mr = m0 + (warp & 3) * 32, nc = n0 + h * 64;
-          if (lane == 0) {
-            if (mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, out + h * 4096);
-            ptx::bulk_commit();
-          }
+          const int mr = m0 + quad * 32, nc = n0 + h * kWHalf + col;
+          if (lane == 0 && mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, out + h * 4096);
           if (n8 >= nc && n8 < nc + 64 && t < P.T) {
             const uint16_t* v =
                 reinterpret_cast<const uint16_t*>(o + ((((n8 - nc) >> 3) ^ (lane & 7)) << 4));
             for (int n = n8; n < P.N; ++n) P.y[(int64_t)t * P.ldy + n] = v[n - n8];
           }
         }
+        if (lane == 0) ptx::bulk_commit();
       } else {
-        // one tile per cluster: part p of K hands each other part its share of the
-        // columns (128 / KS of this thread's), through the drained stages
+        // one tile per cluster: part p of K hands each other part its share of a
+        // thread's 128 columns (32 vectors of 4), through the drained stages, and
+        // each adds the KS shares in rank order
         ptx::cluster_arrive();
         ptx::cluster_wait();
-        const int share = kWHalf / KS, me = warp * 32 + lane;
+        const int sh = 6 - __ffs(KS), share = 1 << sh;      // 32 / KS; KS is a power of two
 #pragma unroll
-        for (int i = 0; i < kWHalf; ++i) {
-          const uint32_t dst = ptx::map_rank(smem, (uint32_t)(i / share) * 2 + half);
-          const uint64_t a = acc[i / 2];
-          ptx::st_cluster_f32(dst + 4 * ((part * share + i % share) * 32 * kWPromote + me),
-                              i & 1 ? ptx::hi32(a) : ptx::lo32(a));
+        for (int j = 0; j < 32; ++j) {
+          const uint64_t u = acc[j / 16][(j % 16) * 2], v = acc[j / 16][(j % 16) * 2 + 1];
+          ptx::st_cluster_v4(ptx::map_rank(smem, (uint32_t)(j >> sh) * 2 + half) +
+                                 16 * ((part * share + (j & (share - 1))) * 32 * kWPromote + tid),
+                             ptx::lo32(u), ptx::hi32(u), ptx::lo32(v), ptx::hi32(v));
         }
         ptx::cluster_arrive();
         ptx::cluster_wait();
-        const float* recv = reinterpret_cast<const float*>(smem);
-        for (int i = 0; i < share; ++i) {
-          float v = 0.f;
-          for (int p = 0; p < KS; ++p) v += recv[(p * share + i) * 32 * kWPromote + me];
-          const int n = n0 + part * share + i;
-          if (t < P.T && n < P.N) P.y[(int64_t)t * P.ldy + n] = Elem<E>::from_f32(v);
+        const float4* recv = reinterpret_cast<const float4*>(smem);
+        for (int j = 0; j < share; ++j) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p = 0; p < KS; ++p) {
+            const float4 u = recv[(p * share + j) * 32 * kWPromote + tid];
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+          }
+          const int jj = part * share + j;
+          const int n = n0 + (jj / 16) * kWHalf + col + (jj % 16) * 4;
+          uint16_t* y = P.y + (int64_t)t * P.ldy + n;
+          if (t < P.T && n + 4 <= P.N) {
+            *reinterpret_cast<uint2*>(y) =
+                make_uint2(Elem<E>::pack2(v.x, v.y), Elem<E>::pack2(v.z, v.w));
+          } else if (t < P.T) {
+            if (n < P.N) y[0] = Elem<E>::from_f32(v.x);
+            if (n + 1 < P.N) y[1] = Elem<E>::from_f32(v.y);
+            if (n + 2 < P.N) y[2] = Elem<E>::from_f32(v.z);
+          }
         }
       }
     }
@@ -429,7 +534,7 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
       for (int c = 0; c < TN / 16; ++c) {
         uint32_t r[16];
         ptx::tc_ld16(trow + b * TN + c * 16, r);
-        ptx::tc_wait_ld();
+        ptx::tc_wait_ld16(r);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           acc[c * 16 + j] = fmaf(sc[c * 16 + j], __uint_as_float(r[j]), acc[c * 16 + j]);
@@ -453,14 +558,14 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
   } else {
     // part p of K hands every other part its share of the tokens (TN / KS),
     // through the drained stages; each adds the KS shares in rank order
-    const int share = TN / KS;
+    const int sh = __ffs(TN) - __ffs(KS), share = 1 << sh;   // TN / KS; both powers of two
     ptx::cluster_arrive();
     ptx::cluster_wait();
     if (warp < 4) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        ptx::st_cluster_f32(ptx::map_rank(smem, (uint32_t)(j / share)) +
-                                4 * ((part * share + j % share) * kNRows + tid),
+        ptx::st_cluster_f32(ptx::map_rank(smem, (uint32_t)(j >> sh)) +
+                                4 * ((part * share + (j & (share - 1))) * kNRows + tid),
                             acc[j]);
     }
     ptx::cluster_arrive();
@@ -521,7 +626,7 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
   WideParams P;
   memset(&P, 0, sizeof(P));
   cudaError_t e = encode_tmap_2d_bytes(&P.tmQ, a.q, a.K, a.T, a.ldq, kBlockK, kWHalf, 128);
-  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, kWHalf, 128);
+  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, 64, 128);
   if (e == cudaSuccess) e = encode_tmap_2d(&P.tmY, dt, a.y, a.N < 8 ? 8 : a.N & ~7, a.T,
                                            (uint64_t)a.ldy * 2, 64, 32, 128);
   if (e != cudaSuccess) return e;

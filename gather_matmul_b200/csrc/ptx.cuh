@@ -64,6 +64,26 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Wait for the phase with the given parity as one block of PTX with its own
+// loop: the compiler sees straight-line code and keeps what is live across it
+// (hundreds of accumulator registers) in place.  Gives up after a million tries
+// (each is suspended for up to a microsecond), or once *stop != 0 (a shared
+// address; set when a wait gives up), and returns false.
+__device__ __forceinline__ bool mbar_wait_asm(uint32_t bar, uint32_t parity, uint32_t stop) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 n, s;\n mov.b32 n, 0;\n"
+      "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra D;\n"
+      " ld.volatile.shared.b32 s, [%3];\n setp.ne.b32 q, s, 0;\n @q bra D;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 1000000;\n @q bra W;\n"
+      " st.volatile.shared.b32 [%3], n;\n"
+      "D:\n selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(stop)
+      : "memory");
+  return ok != 0;
+}
+
 // The same bounded wait for kernels with many waits in a row: it gives up at
 // once when another thread of the CTA has already timed out (*abort != 0), and
 // sets *abort itself on a timeout, so a broken pipeline ends after one
@@ -156,6 +176,30 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// 4-byte asynchronous copy global -> shared, and this thread's arrival on an
+// mbarrier once its earlier ones have landed (one of the barrier's own count).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// Register shares of the warpgroups (every warp of a warpgroup executes it).
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- PDL
 __device__ __forceinline__ void grid_dep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -196,11 +240,51 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+// acc += s2 * {lo, hi}: the pair is named inside the instruction's own block, so
+// that adjacent registers (a tensor-memory load's) are used where they are.
+__device__ __forceinline__ void ffma2_acc(uint64_t& acc, uint64_t s2, uint32_t lo, uint32_t hi) {
+  asm volatile("{\n .reg .b64 t;\n mov.b64 t, {%2, %3};\n fma.rn.f32x2 %0, %1, t, %0;\n}"
+      : "+l"(acc)
+      : "l"(s2), "r"(lo), "r"(hi));
+}
+// 16 of them: acc[i] += s2 * {r[2i], r[2i+1]}
+__device__ __forceinline__ void ffma2_acc16(uint64_t* acc, uint64_t s2, const uint32_t* r) {
+  asm volatile("{\n .reg .b64 t;\n"
+      " mov.b64 t, {%17, %18};\n fma.rn.f32x2 %0, %16, t, %0;\n"
+      " mov.b64 t, {%19, %20};\n fma.rn.f32x2 %1, %16, t, %1;\n"
+      " mov.b64 t, {%21, %22};\n fma.rn.f32x2 %2, %16, t, %2;\n"
+      " mov.b64 t, {%23, %24};\n fma.rn.f32x2 %3, %16, t, %3;\n"
+      " mov.b64 t, {%25, %26};\n fma.rn.f32x2 %4, %16, t, %4;\n"
+      " mov.b64 t, {%27, %28};\n fma.rn.f32x2 %5, %16, t, %5;\n"
+      " mov.b64 t, {%29, %30};\n fma.rn.f32x2 %6, %16, t, %6;\n"
+      " mov.b64 t, {%31, %32};\n fma.rn.f32x2 %7, %16, t, %7;\n"
+      " mov.b64 t, {%33, %34};\n fma.rn.f32x2 %8, %16, t, %8;\n"
+      " mov.b64 t, {%35, %36};\n fma.rn.f32x2 %9, %16, t, %9;\n"
+      " mov.b64 t, {%37, %38};\n fma.rn.f32x2 %10, %16, t, %10;\n"
+      " mov.b64 t, {%39, %40};\n fma.rn.f32x2 %11, %16, t, %11;\n"
+      " mov.b64 t, {%41, %42};\n fma.rn.f32x2 %12, %16, t, %12;\n"
+      " mov.b64 t, {%43, %44};\n fma.rn.f32x2 %13, %16, t, %13;\n"
+      " mov.b64 t, {%45, %46};\n fma.rn.f32x2 %14, %16, t, %14;\n"
+      " mov.b64 t, {%47, %48};\n fma.rn.f32x2 %15, %16, t, %15;\n"
+     "}"
+      : "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7]), "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]), "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15])
+      : "l"(s2), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]));
+}
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
 }
 __device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// One lane of the (converged) warp, the same every time.  Unlike a test of the
+// lane number it tells the compiler that what follows runs in one thread, so
+// that tcgen05 operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(p));
+  return p != 0;
+}
 
 // ---------------------------------------------------------------- tcgen05
 // Tensor memory (TMEM) allocation: one full warp executes these.
@@ -262,6 +346,34 @@ __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Wait for this thread's tensor-memory loads; r names what they wrote, so that
+// no use of it is moved above the wait.
+__device__ __forceinline__ void tc_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tc_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
 __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -317,7 +429,12 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   return a;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
+               "f"(c), "f"(d)
                : "memory");
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
