@@ -47,8 +47,8 @@ __device__ __forceinline__ void drain_copies() {
 // ---------------------------------------------------------------------------
 constexpr int kWTile = 256;                 // tokens and outputs per pair
 constexpr int kWHalf = 128;                 // rows of A and of B that one CTA loads
-constexpr int kWStages = 4;
-constexpr int kWBufs = 4;                   // tensor-memory buffers of 128 columns
+constexpr int kWStages = 5;
+constexpr int kWBufs = 2;                   // tensor-memory buffers of 256 columns
 constexpr int kWPromote = 8;                // promotion warps
 constexpr int kWSlots = 4;                  // groups of 4 blocks whose scales are in shared memory
 constexpr int kWThreads = 32 * (kWPromote + 4);
@@ -58,8 +58,8 @@ constexpr int kWRegsPromote = 232, kWRegsRest = 40;
 struct WideSmem {
   static constexpr int kOperand = kWHalf * kBlockK;             // 16 KB
   static constexpr int kStage = 2 * kOperand;
-  static constexpr int kOut = kWStages * kStage;                // 2 x 4 KB per promotion warp
-  static constexpr int kScale = kOut + kWPromote * 8192;        // per slot: 4 of 128 tokens, 4 of 2 of W
+  static constexpr int kOut = kWStages * kStage;                // 4 KB per promotion warp
+  static constexpr int kScale = kOut + kWPromote * 4096;        // per slot: 4 of 128 tokens, 4 of 2 of W
   static constexpr int kSlot = 16 * (kWHalf + 2);
   static constexpr int kBar = kScale + kWSlots * kSlot;
   static constexpr int kTotal = kBar + 8 * 2 * (kWStages + kWBufs + kWSlots) + 64 + 1024;
@@ -67,7 +67,7 @@ struct WideSmem {
 static_assert(WideSmem::kTotal <= 227 * 1024, "one CTA per SM");
 
 struct WideParams {
-  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128}, {128, 64} bytes; y {64, 32} elements
+  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128} bytes; y {64, 32} elements
   const float* q_scale;
   const float* w_scale;
   uint16_t* y;
@@ -90,7 +90,7 @@ template <typename E>
 __global__ void __launch_bounds__(kWThreads, 1)
 matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   using L = WideSmem;
-  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWHalf);
+  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWTile);
   extern __shared__ char smem_raw[];
   char* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -113,7 +113,7 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   if (tid == 0) {
     for (int s = 0; s < kWStages; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 2);             // both issuing warps
+      ptx::mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < kWBufs; ++b) {
       ptx::mbar_init(&tfull[b], 1);
@@ -160,11 +160,8 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
             const uint32_t bar = bar0 + 8 * s;
             if (half == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
             ptx::tma_load_2d_pair(st, &P.tmQ, kb * kBlockK, m0 + (int)half * kWHalf, bar);
-            // W's rows in two boxes of 64: the MMA of output half h takes rows
-            // h * 64 .. of either CTA, which then are h * 128 + half * 64 .. of the tile
-            ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK, n0 + (int)half * 64, bar);
-            ptx::tma_load_2d_pair(st + L::kOperand + 64 * kBlockK, &P.tmW, kb * kBlockK,
-                                  n0 + kWHalf + (int)half * 64, bar);
+            ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK,
+                                  n0 + (int)half * kWHalf, bar);
           }
         }
         // the last stages' release: no signal may arrive after this CTA has left
@@ -209,30 +206,30 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (half == 0) {
-      // one issuing warp per output half, in the pair's even CTA: the whole warp
-      // runs the loop, an elected thread issues
-      const int h = warp == kWPromote + 1 ? 0 : 1;
+      // the pair's even CTA issues: two warps take the blocks in turn, each with
+      // one of the two buffers, so that one waits while the other's MMAs run; the
+      // whole warp runs the loop, an elected thread the instructions
+      const int b = warp == kWPromote + 1 ? 0 : 1;
       const bool one = ptx::elect_one();
-      const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty + h);
+      const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty + b);
       const uint64_t dq = ptx::umma_desc_kmajor(ptx::smem_u32(smem), 128);
-      const uint64_t dw =
-          ptx::umma_desc_kmajor(ptx::smem_u32(smem) + L::kOperand + h * 64 * kBlockK, 128);
+      const uint64_t dw = dq + (L::kOperand >> 4);
       const uint16_t mask = (uint16_t)(3u << leader);
       const int total = ((n_tiles - first + stride - 1) / stride) * (kb1 - kb0);
-      for (int it = 0; it < total; ++it) {
-        const int s = it % kWStages, b = it & 1;
+      for (int it = b; it < total; it += 2) {
+        const int s = it % kWStages;
         bool ok = ptx::mbar_wait_asm(fu + 8 * s, (it / kWStages) & 1, stop_at);
-        if (it >= 2) ok &= ptx::mbar_wait_asm(te + 16 * b, (it / 2 - 1) & 1, stop_at);
+        ok &= ptx::mbar_wait_asm(te, (it / 2 + 1) & 1, stop_at);
         if (!__all_sync(~0u, ok)) break;
         ptx::tc_fence_after();
         if (one) {
-          const uint32_t d = tmem + (2 * b + h) * kWHalf;
+          const uint32_t d = tmem + b * kWTile;
           const uint64_t qa = dq + (uint32_t)(s * (L::kStage >> 4));
           const uint64_t wa = dw + (uint32_t)(s * (L::kStage >> 4));
 #pragma unroll
           for (int k = 0; k < kBlockK / 32; ++k)
             ptx::tc_mma_f8_pair(d, qa + k * 2, wa + k * 2, kIdesc, k > 0);
-          ptx::tc_commit_pair(&tfull[2 * b + h], mask);
+          ptx::tc_commit_pair(&tfull[b], mask);
           ptx::tc_commit_pair(&empty[s], mask);
         }
         __syncwarp();
@@ -241,13 +238,13 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
     __syncwarp();
   } else {
     ptx::reg_inc<kWRegsPromote>();
-    // promotion: thread = token row; columns 64 * (warp / 4) .. + 63 of either
-    // 128-column half of the tile
-    const int quad = warp & 3, col = (warp >> 2) * 64, row = quad * 32 + lane;
+    // promotion: thread = token row; one 128-column half of the tile (one block
+    // of W) per four warps
+    const int quad = warp & 3, wh = warp >> 2, col = wh * kWHalf, row = quad * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col;
     const uint32_t te = ptx::map_rank(&tempty[0], leader);
     const uint32_t tf = ptx::smem_u32(tfull), sf = ptx::smem_u32(sfull);
-    char* out = smem + L::kOut + warp * 8192;
+    char* out = smem + L::kOut + warp * 4096;
     int it = 0, g = 0;
     for (int tile = first; tile < n_tiles; tile += stride) {
       int m0, n0;
@@ -260,58 +257,46 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
       // 32 columns at a time: the next ones are on their way from tensor memory
       // while the sums of these are formed
       uint32_t r0[32], r1[32];
-      bool ok = ptx::mbar_wait_asm(tf + 16 * (it & 1), (it / 2) & 1, stop_at);
+      bool ok = ptx::mbar_wait_asm(tf + 8 * (it & 1), (it / 2) & 1, stop_at);
       __syncwarp();
       ptx::tc_fence_after();
-      ptx::tc_ld32(trow + (it & 1) * 2 * kWHalf, r0);
+      ptx::tc_ld32(trow + (it & 1) * kWTile, r0);
       for (int kb = kb0; kb < kb1; kb += 4, ++g) {
         const int sl = g % kWSlots, n = min(4, kb1 - kb);
         ok &= ptx::mbar_wait_asm(sf + 8 * sl, (g / kWSlots) & 1, stop_at);
         const float4* sc = reinterpret_cast<const float4*>(smem + L::kScale + sl * L::kSlot);
-        float4 q4 = sc[row];
-        float4 a4 = sc[kWHalf], b4 = sc[kWHalf + 1];
+        const float4 q4 = sc[row];
+        float4 s4 = sc[kWHalf + wh];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sempty[sl]);
+        s4.x *= q4.x; s4.y *= q4.y; s4.z *= q4.z; s4.w *= q4.w;
         for (int j = 0; j < n; ++j, ++it) {
           const int b = it & 1;
-          const uint32_t t0 = trow + b * 2 * kWHalf, tn = trow + (b ^ 1) * 2 * kWHalf;
-          const uint32_t ph = (it / 2) & 1, pn = ((it + 1) / 2) & 1;
-          const float s0 = q4.x * a4.x, s1 = q4.x * b4.x;
-          const uint64_t sa = ptx::pack2(s0, s0), sb = ptx::pack2(s1, s1);
-          q4.x = q4.y; q4.y = q4.z; q4.z = q4.w;
-          a4.x = a4.y; a4.y = a4.z; a4.z = a4.w;
-          b4.x = b4.y; b4.y = b4.z; b4.z = b4.w;
-          const bool more = kb + j + 1 < kb1;
-          // half 0, first 32 columns
+          const uint32_t t0 = trow + b * kWTile;
+          const uint64_t s2 = ptx::pack2(s4.x, s4.x);
+          s4.x = s4.y; s4.y = s4.z; s4.z = s4.w;
           ptx::tc_wait_ld32(r0);
           ptx::tc_ld32(t0 + 32, r1);
-          ptx::ffma2_acc16(acc[0], sa, r0);
-          // half 0, last 32 columns
+          ptx::ffma2_acc16(acc[0], s2, r0);
           ptx::tc_wait_ld32(r1);
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(te + 16 * b);
-          ok &= ptx::mbar_wait_asm(tf + 16 * b + 8, ph, stop_at);
-          __syncwarp();
-          ptx::tc_fence_after();
-          ptx::tc_ld32(t0 + kWHalf, r0);
-          ptx::ffma2_acc16(acc[0] + 16, sa, r1);
-          // half 1, first 32 columns
+          ptx::tc_ld32(t0 + 64, r0);
+          ptx::ffma2_acc16(acc[0] + 16, s2, r1);
           ptx::tc_wait_ld32(r0);
-          ptx::tc_ld32(t0 + kWHalf + 32, r1);
-          ptx::ffma2_acc16(acc[1], sb, r0);
-          // half 1, last 32 columns; the next block's first
+          const bool more = kb + j + 1 < kb1;
+          const uint32_t ready = ptx::mbar_test(tf + 8 * (b ^ 1), ((it + 1) / 2) & 1);
+          ptx::tc_ld32(t0 + 96, r1);
+          ptx::ffma2_acc16(acc[1], s2, r0);
           ptx::tc_wait_ld32(r1);
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(te + 16 * b + 8);
+          if (lane == 0) ptx::mbar_arrive_cluster(te + 8 * b);
           if (more) {
-            ok &= ptx::mbar_wait_asm(tf + 16 * (b ^ 1), pn, stop_at);
+            ok &= ptx::mbar_wait_asm(tf + 8 * (b ^ 1), ((it + 1) / 2) & 1, stop_at, ready);
             __syncwarp();
             ptx::tc_fence_after();
-            ptx::tc_ld32(tn, r0);
+            ptx::tc_ld32(trow + (b ^ 1) * kWTile, r0);
           }
-          ptx::ffma2_acc16(acc[1] + 16, sb, r1);
+          ptx::ffma2_acc16(acc[1] + 16, s2, r1);
         }
       }
       if (!ok) {
@@ -319,16 +304,16 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
         for (int i = 0; i < 64; ++i) acc[i / 32][i % 32] = 0x7fffffff7fffffffull;
       }
       if (KS == 1) {
-        // 32 rows x 64 columns per half through shared memory, in the 128-byte
+        // 32 rows x 64 columns at a time through shared memory, in the 128-byte
         // swizzle the tensor map expects, and out by TMA.  TMA clips at T, but in
         // a row only at whole 16 bytes: the map ends at N rounded down to 8, and
         // the last columns are stored one by one
         const int n8 = P.N & ~7;
-        if (lane == 0) ptx::bulk_wait_read_all();     // the previous tile's copies have left
-        __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          char* o = out + h * 4096 + lane * 128;
+          if (lane == 0) ptx::bulk_wait_read_all();   // the copy before has left
+          __syncwarp();
+          char* o = out + lane * 128;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint4 v;
@@ -340,15 +325,15 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          const int mr = m0 + quad * 32, nc = n0 + h * kWHalf + col;
-          if (lane == 0 && mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, out + h * 4096);
+          const int mr = m0 + quad * 32, nc = n0 + col + h * 64;
+          if (lane == 0 && mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, out);
+          if (lane == 0) ptx::bulk_commit();
           if (n8 >= nc && n8 < nc + 64 && t < P.T) {
             const uint16_t* v =
                 reinterpret_cast<const uint16_t*>(o + ((((n8 - nc) >> 3) ^ (lane & 7)) << 4));
             for (int n = n8; n < P.N; ++n) P.y[(int64_t)t * P.ldy + n] = v[n - n8];
           }
         }
-        if (lane == 0) ptx::bulk_commit();
       } else {
         // one tile per cluster: part p of K hands each other part its share of a
         // thread's 128 columns (32 vectors of 4), through the drained stages, and
@@ -373,7 +358,7 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
             v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
           }
           const int jj = part * share + j;
-          const int n = n0 + (jj / 16) * kWHalf + col + (jj % 16) * 4;
+          const int n = n0 + col + jj * 4;
           uint16_t* y = P.y + (int64_t)t * P.ldy + n;
           if (t < P.T && n + 4 <= P.N) {
             *reinterpret_cast<uint2*>(y) =
@@ -408,18 +393,25 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
 // Narrow: 128 outputs x TN tokens per CTA, K split over a cluster
 // ---------------------------------------------------------------------------
 constexpr int kNRows = 128;
-constexpr int kNThreads = 192;      // warps 0-3 promotion, 4 copies, 5 MMA
+constexpr int kNBufs = 4;           // tensor-memory buffers
+constexpr int kNSlots = 4;          // groups of 4 blocks whose scales are in shared memory
 
 template <int TN>
-struct NarrowSmem {
+struct NarrowShape {
+  static constexpr int kPromote = TN <= 64 ? 4 : 8;                 // promotion warps
+  static constexpr int kCols = TN / (kPromote / 4);                 // columns of each
+  static constexpr int kThreads = 32 * (kPromote + 3);
+  static constexpr int kCtas = TN <= 64 ? 2 : 1;                    // per SM
   static constexpr int kW = kNRows * kBlockK;
   static constexpr int kStage = kW + TN * kBlockK;
-  static constexpr int kStages = TN == 128 ? 3 : (TN == 64 ? 4 : 5);   // two CTAs per SM
-  static constexpr int kBufs = TN == 128 ? 2 : 4;                      // tensor-memory buffers
-  static constexpr int kCols = TN * kBufs;
-  static constexpr int kScale = kStages * kStage;                      // 2 x TN floats
-  static constexpr int kBar = kScale + 2 * TN * 4;
-  static constexpr int kTotal = kBar + 8 * (2 * kStages + 2 * kBufs) + 64 + 1024;
+  static constexpr int kStages = TN == 16 || TN == 128 ? 6 : (TN == 64 ? 4 : 5);
+  static constexpr int kBufs = kNBufs;
+  static constexpr int kTmem = TN * kBufs;
+  static constexpr int kScale = kStages * kStage;                   // per slot [4][TN]
+  static constexpr int kSlot = 4 * 4 * TN;
+  static constexpr int kBar = kScale + kNSlots * kSlot;
+  static constexpr int kTotal = kBar + 8 * 2 * (kStages + kBufs + kNSlots) + 64 + 1024;
+  static_assert(kCtas * (kTotal + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
 struct NarrowParams {
@@ -432,21 +424,25 @@ struct NarrowParams {
 };
 
 template <typename E, int TN>
-__global__ void __launch_bounds__(kNThreads, 2)
+__global__ void __launch_bounds__(NarrowShape<TN>::kThreads, NarrowShape<TN>::kCtas)
 matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
-  using L = NarrowSmem<TN>;
-  constexpr int kS = L::kStages, kB = L::kBufs;
+  using L = NarrowShape<TN>;
+  constexpr int kS = L::kStages, kB = L::kBufs, kPW = L::kPromote, kC = L::kCols;
+  constexpr int kChunk = kC < 32 ? kC : 32;
   constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kNRows, TN);
   extern __shared__ char smem_raw[];
   char* smem = align1024(smem_raw);
-  float* scale = reinterpret_cast<float*>(smem + L::kScale);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* empty = full + kS;
   uint64_t* tfull = empty + kS;
   uint64_t* tempty = tfull + kB;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + kB);
+  uint64_t* sfull = tempty + kB;
+  uint64_t* sempty = sfull + kNSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kNSlots);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t stop_at = ptx::smem_u32(tmem_slot + 1);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);     // uniform in the warp
   const int KS = P.KS, part = (int)ptx::cluster_rank();
   const int unit = blockIdx.x / KS;
   const int n0 = (unit % P.n_tiles) * kNRows, t0 = (unit / P.n_tiles) * TN;
@@ -459,15 +455,19 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
     }
     for (int b = 0; b < kB; ++b) {
       ptx::mbar_init(&tfull[b], 1);
-      ptx::mbar_init(&tempty[b], 4);
+      ptx::mbar_init(&tempty[b], kPW);
+    }
+    for (int s = 0; s < kNSlots; ++s) {
+      ptx::mbar_init(&sfull[s], 32);
+      ptx::mbar_init(&sempty[s], kPW);
     }
     ptx::fence_mbar_init();
     *stop = 0;
     ptx::prefetch_tensormap(&P.tmQ);
     ptx::prefetch_tensormap(&P.tmW);
   }
-  if (warp == 5) {
-    ptx::tmem_alloc(tmem_slot, L::kCols);
+  if (warp == kPW + 1) {
+    ptx::tmem_alloc(tmem_slot, L::kTmem);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -477,12 +477,16 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
 
-  float acc[TN];
-  if (warp == 4) {
+  // promotion: thread = output row, columns = tokens: 32 * (warp % 4) + lane and
+  // kC columns per four warps
+  const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * kC;
+  uint64_t acc[kC / 2];
+  if (warp == kPW) {
     if (lane == 0) {
+      const uint32_t em = ptx::smem_u32(empty);
       for (int i = 0; i < nkb; ++i) {
         const int s = i % kS;
-        if (i >= kS && !ptx::mbar_wait_ff(&empty[s], (i / kS - 1) & 1, stop)) break;
+        if (i >= kS && !ptx::mbar_wait_asm(em + 8 * s, (i / kS - 1) & 1, stop_at)) break;
         char* st = smem + s * L::kStage;
         ptx::mbar_arrive_expect_tx(&full[s], L::kStage);
         ptx::tma_load_2d(st, &P.tmW, (kb0 + i) * kBlockK, n0, &full[s]);
@@ -490,70 +494,119 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
       }
       // the last stages' release: no signal may arrive after this CTA has left
       for (int i = max(nkb - kS, 0); i < nkb; ++i)
-        if (!ptx::mbar_wait_ff(&empty[i % kS], (i / kS) & 1, stop)) break;
+        if (!ptx::mbar_wait_asm(em + 8 * (i % kS), (i / kS) & 1, stop_at)) break;
     }
     __syncwarp();
-  } else if (warp == 5) {
-    if (lane == 0) {
-      const uint32_t sbase = ptx::smem_u32(smem);
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % kS, b = i % kB;
-        if (i >= kB && !ptx::mbar_wait_ff(&tempty[b], (i / kB - 1) & 1, stop)) break;
-        if (!ptx::mbar_wait_ff(&full[s], (i / kS) & 1, stop)) break;
-        ptx::tc_fence_after();
-        const uint32_t wa = sbase + s * L::kStage, qa = wa + L::kW;
+  } else if (warp == kPW + 1) {
+    // the whole warp runs the loop, an elected thread issues
+    const bool one = ptx::elect_one();
+    const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty);
+    const uint64_t dw = ptx::umma_desc_kmajor(ptx::smem_u32(smem), 128);
+    for (int i = 0; i < nkb; ++i) {
+      const int s = i % kS, b = i % kB;
+      bool ok = ptx::mbar_wait_asm(te + 8 * b, (i / kB + 1) & 1, stop_at);
+      ok &= ptx::mbar_wait_asm(fu + 8 * s, (i / kS) & 1, stop_at);
+      if (!__all_sync(~0u, ok)) break;
+      ptx::tc_fence_after();
+      if (one) {
+        const uint64_t wa = dw + (uint32_t)(s * (L::kStage >> 4)), qa = wa + (L::kW >> 4);
 #pragma unroll
         for (int k = 0; k < kBlockK / 32; ++k)
-          ptx::tc_mma_f8(tmem + b * TN, ptx::umma_desc_kmajor(wa + k * 32, 128),
-                         ptx::umma_desc_kmajor(qa + k * 32, 128), kIdesc, k > 0);
-        ptx::tc_commit(&empty[s]);
+          ptx::tc_mma_f8(tmem + b * TN, wa + k * 2, qa + k * 2, kIdesc, k > 0);
         ptx::tc_commit(&tfull[b]);
+        ptx::tc_commit(&empty[s]);
       }
+      __syncwarp();
+    }
+  } else if (warp == kPW + 2) {
+    // scales of the tile's tokens, each times the tile's one scale of W, in
+    // groups of 4 blocks
+    constexpr int kPer = (TN + 31) / 32;
+    const uint32_t se = ptx::smem_u32(sempty);
+    const float* ws = P.w_scale + (int64_t)(n0 / kBlockK) * P.KB + kb0;
+    const float* qs[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      qs[i] = P.q_scale + (int64_t)min(t0 + i * 32 + lane, P.T - 1) * P.KB + kb0;
+    for (int kb = 0, g = 0; kb < nkb; kb += 4, ++g) {
+      const int s = g % kNSlots, n = min(4, nkb - kb);
+      float v[4][kPer];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) {
+          const float w = ws[kb + j];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) v[j][i] = qs[i][kb + j] * w;
+        }
+      if (g >= kNSlots && !ptx::mbar_wait_asm(se + 8 * s, (g / kNSlots - 1) & 1, stop_at)) break;
+      float* dst = reinterpret_cast<float*>(smem + L::kScale + s * L::kSlot);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (j < n && i * 32 + lane < TN) dst[j * TN + i * 32 + lane] = v[j][i];
+      ptx::mbar_arrive(&sfull[s]);
     }
     __syncwarp();
   } else {
-    // promotion: thread = output row, columns = tokens; the tokens' scales of a
-    // block, times the tile's one weight scale, go through shared memory
-    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-    const float* ws = P.w_scale + (int64_t)(n0 / kBlockK) * P.KB + kb0;
-    const float* qs = P.q_scale + (int64_t)min(t0 + tid, P.T - 1) * P.KB + kb0;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+    const uint32_t tf = ptx::smem_u32(tfull), sf = ptx::smem_u32(sfull);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[j] = 0.f;
+    for (int j = 0; j < kC / 2; ++j) acc[j] = 0;
     bool ok = true;
-    float next = tid < TN ? qs[0] * ws[0] : 0.f;
-    for (int i = 0; i < nkb; ++i) {
-      float* sc = scale + (i & 1) * TN;
-      if (tid < TN) sc[tid] = next;
-      if (i + 1 < nkb && tid < TN) next = qs[i + 1] * ws[i + 1];
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      const int b = i % kB;
-      ok = ok && ptx::mbar_wait_ff(&tfull[b], (i / kB) & 1, stop);
-      __syncwarp();
-      ptx::tc_fence_after();
+    for (int kb = 0, g = 0; kb < nkb; kb += 4, ++g) {
+      const int sl = g % kNSlots, n = min(4, nkb - kb);
+      ok &= ptx::mbar_wait_asm(sf + 8 * sl, (g / kNSlots) & 1, stop_at);
+      const char* sc = smem + L::kScale + sl * L::kSlot + c0 * 4;
+      for (int j = 0; j < n; ++j, sc += 4 * TN) {
+        const int b = (kb + j) % kB;
+        const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc);
+        ok &= ptx::mbar_wait_asm(tf + 8 * b, ((kb + j) / kB) & 1, stop_at);
+        __syncwarp();
+        ptx::tc_fence_after();
+        const uint32_t ta = trow + b * TN;
 #pragma unroll
-      for (int c = 0; c < TN / 16; ++c) {
-        uint32_t r[16];
-        ptx::tc_ld16(trow + b * TN + c * 16, r);
-        ptx::tc_wait_ld16(r);
+        for (int c = 0; c < kC / kChunk; ++c) {
+          uint32_t r[kChunk];
+          if constexpr (kChunk == 32) {
+            ptx::tc_ld32(ta + c * 32, r);
+            ptx::tc_wait_ld32(r);
+          } else {
+            ptx::tc_ld16(ta + c * 16, r);
+            ptx::tc_wait_ld16(r);
+          }
+          if (c == kC / kChunk - 1) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&tempty[b]);
+          }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          acc[c * 16 + j] = fmaf(sc[c * 16 + j], __uint_as_float(r[j]), acc[c * 16 + j]);
+          for (int i = 0; i < kChunk / 4; ++i) {
+            const ulonglong2 v = s2[c * (kChunk / 4) + i];
+            uint64_t* a = acc + c * (kChunk / 2) + 2 * i;
+            ptx::ffma2_acc(a[0], v.x, r[4 * i], r[4 * i + 1]);
+            ptx::ffma2_acc(a[1], v.y, r[4 * i + 2], r[4 * i + 3]);
+          }
+        }
       }
-      ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&tempty[b]);
+      if (lane == 0) ptx::mbar_arrive(&sempty[sl]);
     }
     if (!ok) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[j] = __int_as_float(0x7fffffff);
+      for (int j = 0; j < kC / 2; ++j) acc[j] = 0x7fffffff7fffffffull;
     }
   }
-  const int n = n0 + tid;
+  const int n = n0 + row;
   if (KS == 1) {
-    if (warp < 4 && n < P.N) {
+    if (warp < kPW && n < P.N) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        if (t0 + j < P.T) P.y[(int64_t)(t0 + j) * P.ldy + n] = Elem<E>::from_f32(acc[j]);
+      for (int j = 0; j < kC; ++j) {
+        const int t = t0 + c0 + j;
+        if (t < P.T)
+          P.y[(int64_t)t * P.ldy + n] =
+              Elem<E>::from_f32(j & 1 ? ptx::hi32(acc[j / 2]) : ptx::lo32(acc[j / 2]));
+      }
     }
   } else {
     // part p of K hands every other part its share of the tokens (TN / KS),
@@ -561,22 +614,22 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
     const int sh = __ffs(TN) - __ffs(KS), share = 1 << sh;   // TN / KS; both powers of two
     ptx::cluster_arrive();
     ptx::cluster_wait();
-    if (warp < 4) {
+    if (warp < kPW) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        ptx::st_cluster_f32(ptx::map_rank(smem, (uint32_t)(j >> sh)) +
-                                4 * ((part * share + (j & (share - 1))) * kNRows + tid),
-                            acc[j]);
+      for (int j = 0; j < kC; ++j)
+        ptx::st_cluster_f32(ptx::map_rank(smem, (uint32_t)((c0 + j) >> sh)) +
+                                4 * ((part * share + ((c0 + j) & (share - 1))) * kNRows + row),
+                            j & 1 ? ptx::hi32(acc[j / 2]) : ptx::lo32(acc[j / 2]));
     }
     ptx::cluster_arrive();
     ptx::cluster_wait();
     const float* recv = reinterpret_cast<const float*>(smem);
-    if (warp < 4 && n < P.N) {
-      for (int j = 0; j < share; ++j) {
+    if (warp < kPW && n < P.N) {
+      for (int j = warp >> 2; j < share; j += kPW / 4) {
         const int t = t0 + part * share + j;
         if (t >= P.T) break;
         float v = 0.f;
-        for (int p = 0; p < KS; ++p) v += recv[(p * share + j) * kNRows + tid];
+        for (int p = 0; p < KS; ++p) v += recv[(p * share + j) * kNRows + row];
         P.y[(int64_t)t * P.ldy + n] = Elem<E>::from_f32(v);
       }
     }
@@ -584,7 +637,7 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
   if (*stop && tid == 0) drain_copies();
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 5) ptx::tmem_dealloc(tmem, L::kCols);
+  if (warp == kPW + 1) ptx::tmem_dealloc(tmem, L::kTmem);
 }
 
 int sm_count() {
@@ -626,7 +679,7 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
   WideParams P;
   memset(&P, 0, sizeof(P));
   cudaError_t e = encode_tmap_2d_bytes(&P.tmQ, a.q, a.K, a.T, a.ldq, kBlockK, kWHalf, 128);
-  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, 64, 128);
+  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, kWHalf, 128);
   if (e == cudaSuccess) e = encode_tmap_2d(&P.tmY, dt, a.y, a.N < 8 ? 8 : a.N & ~7, a.T,
                                            (uint64_t)a.ldy * 2, 64, 32, 128);
   if (e != cudaSuccess) return e;
@@ -641,8 +694,12 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
   P.m_tiles = (a.T + kWTile - 1) / kWTile;
   P.n_tiles = (a.N + kWTile - 1) / kWTile;
   const int tiles = P.m_tiles * P.n_tiles, pairs = sm_count() / 2;
-  int KS = 1;
-  while (KS < 4 && tiles * KS * 2 <= pairs && P.KB >= 4 * KS) KS *= 2;
+  // Two pairs per tile where at most half of them would work: 18.2 us against
+  // 19.6 at 256 x 4096 x 4096, 37.5 against 54.6 at 512 x 4096 x 14336.  The
+  // exchange of a tile's sums costs about 8 us, so not for short K (7.3 us
+  // against 12 at 8192 x 128 x 512), and four parts never pay (29 against 18 us
+  // at 4096 x 256 x 4096).
+  const int KS = tiles * 2 <= pairs && P.KB >= 16 ? 2 : 1;
   P.KS = KS;
   const int clusters = KS > 1 ? tiles : (tiles < pairs ? tiles : pairs);
   return cluster_launch(matmul_fp8_wide_kernel<E>, P, clusters * 2 * KS, 2 * KS, kWThreads,
@@ -666,18 +723,44 @@ cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
   P.n_tiles = (a.N + kNRows - 1) / kNRows;
   const int units = P.n_tiles * ((a.T + TN - 1) / TN);
   int KS = 1;
-  while (KS < 8 && units * KS * 2 <= 2 * sm_count() && P.KB >= 4 * KS) KS *= 2;
+  // K split until the CTAs fill the device, two blocks at least for each part.
+  // The first split pays for the exchange only if it fills idle SMs or shortens
+  // a long K: 12.8 us unsplit against 14.1 in two at 48 x 8192 x 4096 (128 CTAs),
+  // but 18.8 in two against 20.9 at 256 x 2048 x 8192.
+  const int room = NarrowShape<TN>::kCtas * sm_count();
+  if (units * 2 <= sm_count() || P.KB >= 48)
+    while (KS < 8 && units * KS * 2 <= room && P.KB >= 4 * KS) KS *= 2;
   P.KS = KS;
-  return cluster_launch(matmul_fp8_narrow_kernel<E, TN>, P, units * KS, KS, kNThreads,
-                        NarrowSmem<TN>::kTotal, st);
+  return cluster_launch(matmul_fp8_narrow_kernel<E, TN>, P, units * KS, KS, 
+                        NarrowShape<TN>::kThreads, NarrowShape<TN>::kTotal, st);
 }
 
 template <typename E>
 cudaError_t matmul_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) {
+  // The tile by how many CTAs it makes.  Measured (us, K = 4096 unless given):
+  //   T x N           16     32     64    128    256 (wide)
+  //   1 x 4096        6.9    7.3    9.0   12     33
+  //   64 x 8192      13.9   12.8   18.2   18.2   50
+  //   64 x 28672     62.6   36.4   27.7   36.4   67
+  //   128 x 4096     13.9   12.6   15.2   13.7   18
+  //   128 x 28672   114     67.9   50.8   40.0   51
+  //   256 x 4096             15.8  18.4   18.9   18.2
+  //   256 x 8192             29.8  26.2   20.2   19.9
+  //   256 x 14336            54.0  50.2   39.4   21.7
+  //   512 x 4096 x 14336           76.0   52.6   37.5
+  // Tiles of 32 tokens are the best while two CTAs per SM hold them all, 128
+  // while one does; past that only the wide kernel's reuse of both operands
+  // keeps up.  Few tiles of a long K go to the wide kernel, whose two parts of
+  // K then fill the device.
+  const int sms = sm_count(), n = (a.N + kNRows - 1) / kNRows;
+  const auto units = [&](int tn) { return (int64_t)n * ((a.T + tn - 1) / tn); };
+  const int64_t tiles = (int64_t)((a.N + kWTile - 1) / kWTile) * ((a.T + kWTile - 1) / kWTile);
   if (a.T <= 16) return narrow_launch<E, 16>(a, st);
-  if (a.T <= 32) return narrow_launch<E, 32>(a, st);
+  if (a.T <= 32 || units(32) <= sms) return narrow_launch<E, 32>(a, st);
+  if (a.T > 128 && 4 * tiles <= sms && a.K >= 40 * kBlockK) return wide_launch<E>(dt, a, st);
+  if (units(32) <= 2 * sms) return narrow_launch<E, 32>(a, st);
   if (a.T <= 64) return narrow_launch<E, 64>(a, st);
-  if (a.T <= 128) return narrow_launch<E, 128>(a, st);
+  if (a.T <= 128 || units(128) <= sms) return narrow_launch<E, 128>(a, st);
   return wide_launch<E>(dt, a, st);
 }
 

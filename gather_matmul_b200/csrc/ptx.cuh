@@ -64,22 +64,36 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Whether the phase has completed, without suspending the thread.
+__device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
 // Wait for the phase with the given parity as one block of PTX with its own
 // loop: the compiler sees straight-line code and keeps what is live across it
 // (hundreds of accumulator registers) in place.  Gives up after a million tries
 // (each is suspended for up to a microsecond), or once *stop != 0 (a shared
-// address; set when a wait gives up), and returns false.
-__device__ __forceinline__ bool mbar_wait_asm(uint32_t bar, uint32_t parity, uint32_t stop) {
+// address; set when a wait gives up), and returns false.  `ready`: an earlier
+// mbar_test of the same phase (its latency then lies behind the work between).
+__device__ __forceinline__ bool mbar_wait_asm(uint32_t bar, uint32_t parity, uint32_t stop,
+                                              uint32_t ready = 0) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b32 n, s;\n mov.b32 n, 0;\n"
+      "{\n .reg .pred p, q;\n .reg .b32 n, s;\n mov.b32 n, 0;\n setp.ne.b32 p, %4, 0;\n"
+      " @p bra D;\n"
       "W:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra D;\n"
       " ld.volatile.shared.b32 s, [%3];\n setp.ne.b32 q, s, 0;\n @q bra D;\n"
       " add.u32 n, n, 1;\n setp.lt.u32 q, n, 1000000;\n @q bra W;\n"
       " st.volatile.shared.b32 [%3], n;\n"
       "D:\n selp.b32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(stop)
+      : "r"(bar), "r"(parity), "r"(stop), "r"(ready)
       : "memory");
   return ok != 0;
 }
@@ -146,6 +160,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+// The tile's bytes into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 // Four rows (row0..row3, each box-width elements from column x) of a 2-D
 // tensor into consecutive rows of shared memory, with the map's swizzle; the
