@@ -112,6 +112,7 @@ lora_status rope_impl(lora_dtype dtype, int T, int dim, int rot, int n_slices,
   a.inv_freq = inv_freq;
   a.attn_scale = attn_scale;
   a.eps = eps;
+  a.inv_dim = 1.f / (float)dim;
   a.interleaved = interleaved != 0;
   cudaGetLastError();
   return from_cuda(launch_rope(dtype, a, norm, (cudaStream_t)stream));

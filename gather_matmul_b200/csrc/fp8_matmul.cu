@@ -19,6 +19,7 @@
 // makes its outputs NaN.
 #include <string.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -641,7 +642,7 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
 }
 
 int sm_count() {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
   if (cache[dev] == 0) {
@@ -653,11 +654,21 @@ int sm_count() {
   return cache[dev];
 }
 
-template <typename Kern, typename Params>
-cudaError_t cluster_launch(Kern kern, const Params& P, unsigned grid, unsigned cluster,
+template <auto kKernel, typename Params>
+cudaError_t cluster_launch(const Params& P, unsigned grid, unsigned cluster,
                            unsigned threads, size_t smem, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the shared-memory limit is a property of the kernel on a device: set it on
+  // the first launch there only
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit) || bit == 0) {
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
@@ -671,7 +682,7 @@ cudaError_t cluster_launch(Kern kern, const Params& P, unsigned grid, unsigned c
   attr[1] = pdl_attribute();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return counted_launch(cudaLaunchKernelEx(&cfg, kern, P));
+  return counted_launch(cudaLaunchKernelEx(&cfg, kKernel, P));
 }
 
 template <typename E>
@@ -702,8 +713,8 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
   const int KS = tiles * 2 <= pairs && P.KB >= 16 ? 2 : 1;
   P.KS = KS;
   const int clusters = KS > 1 ? tiles : (tiles < pairs ? tiles : pairs);
-  return cluster_launch(matmul_fp8_wide_kernel<E>, P, clusters * 2 * KS, 2 * KS, kWThreads,
-                        WideSmem::kTotal, st);
+  return cluster_launch<matmul_fp8_wide_kernel<E>>(P, clusters * 2 * KS, 2 * KS, kWThreads,
+                                                   WideSmem::kTotal, st);
 }
 
 template <typename E, int TN>
@@ -731,8 +742,8 @@ cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
   if (units * 2 <= sm_count() || P.KB >= 48)
     while (KS < 8 && units * KS * 2 <= room && P.KB >= 4 * KS) KS *= 2;
   P.KS = KS;
-  return cluster_launch(matmul_fp8_narrow_kernel<E, TN>, P, units * KS, KS, 
-                        NarrowShape<TN>::kThreads, NarrowShape<TN>::kTotal, st);
+  return cluster_launch<matmul_fp8_narrow_kernel<E, TN>>(
+      P, units * KS, KS, NarrowShape<TN>::kThreads, NarrowShape<TN>::kTotal, st);
 }
 
 template <typename E>

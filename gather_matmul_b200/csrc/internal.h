@@ -98,7 +98,7 @@ struct RopeArgs {
   int n_slices, T, dim, rot;
   const int64_t* positions;
   const double* inv_freq;
-  float attn_scale, eps;
+  float attn_scale, eps, inv_dim;      // inv_dim: 1 / dim
   int interleaved;
 };
 

@@ -8,10 +8,12 @@
 // per token for all its heads, into shared memory, while its loads of the
 // heads are in flight.
 //
-// Bound: memory (2 bytes read and 2 written per element).  A group of L lanes
-// holds one head: each lane the two vectors of V elements that its pairs join,
-// so a half-split rotation needs no exchange between lanes, and the norm needs
-// one sum over the L lanes.
+// Bound: memory (2 bytes read and 2 written per element; 30 us at 8192 tokens of
+// 32 + 8 heads of 128, 5.6 TB/s).  A group of L lanes holds one head: each lane
+// the two vectors of V elements that its pairs join, so a half-split rotation
+// needs no exchange between lanes, and the norm needs one sum over the L lanes.
+// The order of the table decides much: with (cos, sin) pairs in the order of the
+// pairs, lanes read it with 4-way bank conflicts, and the same call took 35 us.
 #include <math.h>
 
 #include <type_traits>
@@ -29,6 +31,11 @@ template <> struct Vec<8> { typedef uint4 type; };
 template <> struct Vec<4> { typedef uint2 type; };
 template <> struct Vec<2> { typedef uint32_t type; };
 template <> struct Vec<1> { typedef uint16_t type; };
+
+template <int W> struct Floats;
+template <> struct Floats<4> { typedef float4 type; };
+template <> struct Floats<2> { typedef float2 type; };
+template <> struct Floats<1> { typedef float type; };
 
 template <typename E, int V>
 __device__ __forceinline__ void unpack(const typename Vec<V>::type& v, float* f) {
@@ -54,33 +61,53 @@ constexpr int kRThreads = 512;   // most threads of a CTA
 struct RopeGrid {
   int L;            // lanes per head, a power of two up to 32
   int heads_cta;    // heads per CTA and token
-  int tokens_cta;   // tokens per CTA
+  int slots;        // groups of TPT tokens per CTA
 };
 
 // ITEMS pair vectors per lane: units of V pairs u, u + L, ... of the head's
-// dim / 2 / V; the first rot / 2 / V of them are rotated.
-template <typename E, int V, int ITEMS, bool INTER, bool NORM>
+// dim / 2 / V; the first rot / 2 / V of them are rotated.  TPT consecutive
+// tokens per thread, all of whose loads are in flight at once.
+template <typename E, int V, int ITEMS, int TPT, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kRThreads) rope_kernel(const RopeArgs a, const RopeGrid G) {
   typedef typename Vec<V>::type vec;
-  extern __shared__ float2 cs[];          // [tokens_cta][rot / 2]
+  extern __shared__ float4 cs4[];         // [slots * TPT][rot]
+  float* cs = reinterpret_cast<float*>(cs4);
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
   const int h = a.rot / 2, pass = (a.dim - a.rot) / 2;
   const int units = a.dim / 2 / V, turned = h / V;
+  // A token's table: the W cosines (then sines) of a unit that one access takes lie
+  // side by side, units next to each other, so that lanes read without conflicts.
+  constexpr int W = V < 4 ? V : 4;
+  const auto put = [&](float* t, int i, float c, float sn) {
+    const int u = i / V, j = i % V;
+    t[((j / W) * turned + u) * W + j % W] = c;
+    t[((V / W + j / W) * turned + u) * W + j % W] = sn;
+  };
+  const auto get = [&](const float* t, int u, float* c, float* sn) {
+    typedef typename Floats<W>::type vf;
+#pragma unroll
+    for (int q = 0; q < V / W; ++q) {
+      *reinterpret_cast<vf*>(c + q * W) = *reinterpret_cast<const vf*>(t + (q * turned + u) * W);
+      *reinterpret_cast<vf*>(sn + q * W) =
+          *reinterpret_cast<const vf*>(t + ((V / W + q) * turned + u) * W);
+    }
+  };
   const int n_heads = a.head_end[a.n_slices - 1];
-  const int slot = threadIdx.x / G.L, l = threadIdx.x % G.L;
-  const int tok = slot / G.heads_cta;
-  const int64_t t0 = (int64_t)blockIdx.x * G.tokens_cta;
-  const int64_t t = t0 + tok;
-  const int head = blockIdx.y * G.heads_cta + slot % G.heads_cta;
-  const bool active = tok < G.tokens_cta && t < a.T && head < n_heads;
+  const int place = threadIdx.x / G.L, l = threadIdx.x % G.L;
+  const int slot = place / G.heads_cta;
+  const int64_t first = (int64_t)blockIdx.x * G.slots * TPT;
+  const int64_t t0 = first + slot * TPT;
+  const int head = blockIdx.y * G.heads_cta + place % G.heads_cta;
+  const bool active = slot < G.slots && t0 < a.T && head < n_heads;
   int s = 0, in_slice = head;
   if (active) {
     while (head >= a.head_end[s]) ++s;
     in_slice = head - (s > 0 ? a.head_end[s - 1] : 0);
   }
-  const E* x = static_cast<const E*>(a.x) + t * a.ldx + a.x_off[s] + (int64_t)in_slice * a.dim;
-  vec va[ITEMS], vb[ITEMS];
+  const E* x = static_cast<const E*>(a.x) + t0 * a.ldx + a.x_off[s] + (int64_t)in_slice * a.dim;
+  const E* w = NORM ? static_cast<const E*>(a.weight[s]) : nullptr;
+  vec va[TPT][ITEMS], vb[TPT][ITEMS], wa[ITEMS], wb[ITEMS];
   int ea[ITEMS], eb[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
@@ -92,117 +119,140 @@ __global__ void __launch_bounds__(kRThreads) rope_kernel(const RopeArgs a, const
       ea[i] = u < turned ? u * V : a.rot + (u - turned) * V;
       eb[i] = ea[i] + (u < turned ? h : pass);
     }
-    va[i] = vec();
-    vb[i] = vec();
-    if (active && u < units) {
-      va[i] = *reinterpret_cast<const vec*>(x + ea[i]);
-      vb[i] = *reinterpret_cast<const vec*>(x + eb[i]);
+#pragma unroll
+    for (int k = 0; k < TPT; ++k) {
+      va[k][i] = vec();
+      vb[k][i] = vec();
+      if (active && u < units && t0 + k < a.T) {
+        va[k][i] = *reinterpret_cast<const vec*>(x + k * a.ldx + ea[i]);
+        vb[k][i] = *reinterpret_cast<const vec*>(x + k * a.ldx + eb[i]);
+      }
+    }
+    if constexpr (NORM) {
+      wa[i] = vec();
+      wb[i] = vec();
+      if (active && w != nullptr && u < units) {
+        wa[i] = *reinterpret_cast<const vec*>(w + ea[i]);
+        wb[i] = *reinterpret_cast<const vec*>(w + eb[i]);
+      }
     }
   }
-  for (int i = threadIdx.x; i < G.tokens_cta * h; i += blockDim.x) {
-    const int64_t tt = t0 + i / h;
+  for (int i = threadIdx.x; i < G.slots * TPT * h; i += blockDim.x) {
+    const int64_t tt = first + i / h;
     if (tt >= a.T) break;
     const double turns = (double)a.positions[tt] * (a.inv_freq[i % h] * 0.15915494309189533577);
     float sn, c;
     sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
-    cs[i] = make_float2(c * a.attn_scale, sn * a.attn_scale);
+    put(cs + (i / h) * a.rot, i % h, c * a.attn_scale, sn * a.attn_scale);
   }
   __syncthreads();
-  float fa[ITEMS][V], fb[ITEMS][V];
+  E* y = static_cast<E*>(a.y) + t0 * a.ldy + a.y_off[s] + (int64_t)in_slice * a.dim;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    unpack<E, V>(va[i], fa[i]);
-    unpack<E, V>(vb[i], fb[i]);
-  }
-  if constexpr (NORM) {
-    float sum = 0.f;
+  for (int k = 0; k < TPT; ++k) {
+    float fa[ITEMS][V], fb[ITEMS][V];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
+    for (int i = 0; i < ITEMS; ++i) {
+      unpack<E, V>(va[k][i], fa[i]);
+      unpack<E, V>(vb[k][i], fb[i]);
+    }
+    if constexpr (NORM) {
+      float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum = fmaf(fa[i][j], fa[i][j], fmaf(fb[i][j], fb[i][j], sum));
-    for (int o = G.L >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const E* w = static_cast<const E*>(a.weight[s]);
-    if (active && w != nullptr) {
-      const float inv = 1.f / sqrtf(sum / (float)a.dim + a.eps);
+      for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        if (l + i * G.L < units) {
-          float wa[V], wb[V];
-          unpack<E, V>(*reinterpret_cast<const vec*>(w + ea[i]), wa);
-          unpack<E, V>(*reinterpret_cast<const vec*>(w + eb[i]), wb);
+        for (int j = 0; j < V; ++j) sum = fmaf(fa[i][j], fa[i][j], fmaf(fb[i][j], fb[i][j], sum));
+      for (int o = G.L >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if (w != nullptr) {
+        const float inv = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          float ga[V], gb[V];
+          unpack<E, V>(wa[i], ga);
+          unpack<E, V>(wb[i], gb);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            fa[i][j] *= inv * wa[j];
-            fb[i][j] *= inv * wb[j];
+            fa[i][j] *= inv * ga[j];
+            fb[i][j] *= inv * gb[j];
           }
         }
       }
     }
-  }
-  if (!active) return;
-  E* y = static_cast<E*>(a.y) + t * a.ldy + a.y_off[s] + (int64_t)in_slice * a.dim;
+    if (!active || t0 + k >= a.T) continue;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int u = l + i * G.L;
-    if (u < units) {
-      if (u < turned) {
-        const float2* c = cs + tok * h + u * V;
-        if constexpr (INTER && V > 1) {
-          // pairs lie inside each vector: V / 2 in va, V / 2 in vb
+    for (int i = 0; i < ITEMS; ++i) {
+      const int u = l + i * G.L;
+      if (u < units) {
+        if (u < turned) {
+          alignas(16) float co[V], si[V];
+          get(cs + (slot * TPT + k) * a.rot, u, co, si);
+          if constexpr (INTER && V > 1) {
+            // pairs lie inside each vector: V / 2 in va, V / 2 in vb
 #pragma unroll
-          for (int j = 0; j < V / 2; ++j) {
-            const float2 p = c[j], q = c[j + V / 2];
-            const float a0 = fa[i][2 * j], a1 = fa[i][2 * j + 1];
-            const float b0 = fb[i][2 * j], b1 = fb[i][2 * j + 1];
-            fa[i][2 * j] = a0 * p.x - a1 * p.y;
-            fa[i][2 * j + 1] = a1 * p.x + a0 * p.y;
-            fb[i][2 * j] = b0 * q.x - b1 * q.y;
-            fb[i][2 * j + 1] = b1 * q.x + b0 * q.y;
-          }
-        } else {
+            for (int j = 0; j < V / 2; ++j) {
+              
+              const float a0 = fa[i][2 * j], a1 = fa[i][2 * j + 1];
+              const float b0 = fb[i][2 * j], b1 = fb[i][2 * j + 1];
+              fa[i][2 * j] = a0 * co[j] - a1 * si[j];
+              fa[i][2 * j + 1] = a1 * co[j] + a0 * si[j];
+              fb[i][2 * j] = b0 * co[j + V / 2] - b1 * si[j + V / 2];
+              fb[i][2 * j + 1] = b1 * co[j + V / 2] + b0 * si[j + V / 2];
+            }
+          } else {
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float2 p = c[j];
-            const float u0 = fa[i][j], u1 = fb[i][j];
-            fa[i][j] = u0 * p.x - u1 * p.y;
-            fb[i][j] = u1 * p.x + u0 * p.y;
+            for (int j = 0; j < V; ++j) {
+              
+              const float u0 = fa[i][j], u1 = fb[i][j];
+              fa[i][j] = u0 * co[j] - u1 * si[j];
+              fb[i][j] = u1 * co[j] + u0 * si[j];
+            }
           }
         }
+        *reinterpret_cast<vec*>(y + k * a.ldy + ea[i]) = pack<E, V>(fa[i]);
+        *reinterpret_cast<vec*>(y + k * a.ldy + eb[i]) = pack<E, V>(fb[i]);
       }
-      *reinterpret_cast<vec*>(y + ea[i]) = pack<E, V>(fa[i]);
-      *reinterpret_cast<vec*>(y + eb[i]) = pack<E, V>(fb[i]);
     }
   }
 }
 
-template <typename E, int V, int ITEMS, bool INTER>
+template <typename E, int V, int ITEMS, int TPT, bool INTER>
 cudaError_t rope_launch(const RopeArgs& a, bool norm, cudaStream_t st) {
   const int units = a.dim / 2 / V, n_heads = a.head_end[a.n_slices - 1];
   RopeGrid G;
   G.L = 1;
   while (G.L < 32 && G.L < units) G.L *= 2;
-  const int slots = kRThreads / G.L;
-  const int chunks = (n_heads + slots - 1) / slots;
+  const int places = kRThreads / G.L;
+  const int chunks = (n_heads + places - 1) / places;
   G.heads_cta = (n_heads + chunks - 1) / chunks;
-  G.tokens_cta = chunks > 1 ? 1 : min(max(256 / G.L / n_heads, 1), a.T);
-  const int threads = (G.heads_cta * G.tokens_cta * G.L + 31) / 32 * 32;
+  const int groups = (a.T + TPT - 1) / TPT;
+  G.slots = chunks > 1 ? 1 : min(max(256 / G.L / n_heads, 1), groups);
+  const int threads = (G.heads_cta * G.slots * G.L + 31) / 32 * 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.T + G.tokens_cta - 1) / G.tokens_cta, chunks, 1);
+  cfg.gridDim = dim3((groups + G.slots - 1) / G.slots, chunks, 1);
   cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(float2) * (size_t)G.tokens_cta * (a.rot / 2);
+  cfg.dynamicSmemBytes = sizeof(float2) * (size_t)G.slots * TPT * (a.rot / 2);
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return counted_launch(
-      norm ? cudaLaunchKernelEx(&cfg, rope_kernel<E, V, ITEMS, INTER, true>, a, G)
-           : cudaLaunchKernelEx(&cfg, rope_kernel<E, V, ITEMS, INTER, false>, a, G));
+      norm ? cudaLaunchKernelEx(&cfg, rope_kernel<E, V, ITEMS, TPT, INTER, true>, a, G)
+           : cudaLaunchKernelEx(&cfg, rope_kernel<E, V, ITEMS, TPT, INTER, false>, a, G));
 }
 
+template <typename E, int V, int ITEMS, int TPT>
+cudaError_t rope_tokens(const RopeArgs& a, bool norm, cudaStream_t st) {
+  return a.interleaved ? rope_launch<E, V, ITEMS, TPT, true>(a, norm, st)
+                       : rope_launch<E, V, ITEMS, TPT, false>(a, norm, st);
+}
+
+// Two tokens per thread once that leaves several CTAs per SM (about 320 threads
+// each): 30.0 us against 33.8 at 8192 tokens of 40 heads of 128 (38.1 against
+// 47.2 with norms; four tokens 31.0 and 38.8), 3.6 against 3.3 at 512 tokens.
 template <typename E, int V, int ITEMS>
 cudaError_t rope_layout(const RopeArgs& a, bool norm, cudaStream_t st) {
-  return a.interleaved ? rope_launch<E, V, ITEMS, true>(a, norm, st)
-                       : rope_launch<E, V, ITEMS, false>(a, norm, st);
+  const int64_t lanes = (int64_t)a.T * a.head_end[a.n_slices - 1] * (a.dim / 2 / V / ITEMS);
+  return lanes >= 2 * 6 * 148 * 320 ? rope_tokens<E, V, ITEMS, 2>(a, norm, st)
+                                    : rope_tokens<E, V, ITEMS, 1>(a, norm, st);
 }
 
 // The widest vector whose length divides both the rotated pairs and the rest:

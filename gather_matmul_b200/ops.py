@@ -285,29 +285,35 @@ def shrink_noalloc(x: torch.Tensor, A: Sequence[torch.Tensor], idx: torch.Tensor
 # CUDA device.
 # ---------------------------------------------------------------------------
 _FP8 = torch.float8_e4m3fn
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _here(*tensors):
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+def _here(stream, *tensors):
+    """The stream handle to launch on, once every tensor lies on the current device."""
+    dev = tensors[0].get_device()
     for t in tensors:
         if t.get_device() != dev:
-            raise ValueError("tensors must lie on the current CUDA device")
+            dev = -1
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must lie on the current CUDA device")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
 def _rows(t, name, dtype=None):
     """Row stride of a 2-D tensor with unit column stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() > 0 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.shape[0] > 1:
-        return t.stride(0)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
     # a single row has no next one: any stride that the alignment rules take
-    return -(-max(t.shape[1], 1) // 16) * 16
+    return stride[0] if shape[0] > 1 else -(-max(shape[1], 1) // 16) * 16
 
 
 def _scales(t, name, rows, K):
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (rows, -(-K // 128)):
+    if t.dtype is not torch.float32 or not t.is_contiguous() or t.shape != (rows, -(-K // 128)):
         raise TypeError(f"{name} must be a contiguous float32 tensor of {rows} x {-(-K // 128)}")
 
 
@@ -324,10 +330,9 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_ro
     if q.shape != x.shape:
         raise ValueError("q must have the shape of x")
     _scales(scale, "scale", -(-T // block_rows) if block_rows > 0 else 0, K)
-    _here(x, q, scale)
+    st = _here(stream, x, q, scale)
     _check("lora_quantize_fp8", _lib.load().lora_quantize_fp8(
-        _dtype(x), T, K, block_rows, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(),
-        _stream(stream)))
+        _dtype(x), T, K, block_rows, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), st))
     return q, scale
 
 
@@ -343,10 +348,10 @@ def matmul_fp8(q: torch.Tensor, q_scale: torch.Tensor, W: torch.Tensor, w_scale:
         raise ValueError("shapes must be q [T, K], W [N, K], y [T, N]")
     _scales(q_scale, "q_scale", T, K)
     _scales(w_scale, "w_scale", -(-N // 128), K)
-    _here(q, q_scale, W, w_scale, y)
+    st = _here(stream, q, q_scale, W, w_scale, y)
     _check("lora_matmul_fp8", _lib.load().lora_matmul_fp8(
         _dtype(y), T, N, K, q.data_ptr(), ldq, q_scale.data_ptr(), W.data_ptr(), ldw,
-        w_scale.data_ptr(), y.data_ptr(), ldy, _stream(stream)))
+        w_scale.data_ptr(), y.data_ptr(), ldy, st))
     return y
 
 
@@ -372,10 +377,10 @@ def linear_fp8(x: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, y: torch
     _scales(w_scale, "w_scale", -(-N // 128), K)
     if not work.is_contiguous():
         raise ValueError("work must be contiguous")
-    _here(x, W, w_scale, y, work)
+    st = _here(stream, x, W, w_scale, y, work)
     _check("lora_linear_fp8", _lib.load().lora_linear_fp8(
         _dtype(x), T, N, K, x.data_ptr(), ldx, W.data_ptr(), ldw, w_scale.data_ptr(), y.data_ptr(),
-        ldy, work.data_ptr(), work.numel() * work.element_size(), _stream(stream)))
+        ldy, work.data_ptr(), work.numel() * work.element_size(), st))
     return y
 
 
@@ -432,12 +437,12 @@ def rope(x: torch.Tensor, y: torch.Tensor, heads: Sequence[int], head_dim: int,
     offsets (in place).  positions: int64 [T]; inv_freq, attn_scale from
     rope_frequencies()."""
     T, ldx, ldy, h = _rope_common(x, y, heads, positions, inv_freq)
-    _here(x, y, positions, inv_freq)
+    st = _here(stream, x, y, positions, inv_freq)
     _check("lora_rope", _lib.load().lora_rope(
         _dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx,
         _offsets(x, heads, head_dim, x_col_off), y.data_ptr(), ldy,
         _offsets(y, heads, head_dim, y_col_off), positions.data_ptr(), inv_freq.data_ptr(),
-        attn_scale, bool(interleaved), _stream(stream)))
+        attn_scale, bool(interleaved), st))
     return y
 
 
@@ -455,13 +460,13 @@ def norm_rope(x: torch.Tensor, weights, y: torch.Tensor, heads: Sequence[int], h
         if w is not None and (w.dtype != x.dtype or not w.is_contiguous() or
                               w.numel() != head_dim):
             raise TypeError("a weight must be a contiguous tensor of head_dim elements of x's dtype")
-    _here(x, y, positions, inv_freq, *[w for w in weights if w is not None])
+    st = _here(stream, x, y, positions, inv_freq, *[w for w in weights if w is not None])
     ws = (ctypes.c_void_p * len(weights))(*[None if w is None else w.data_ptr() for w in weights])
     _check("lora_norm_rope", _lib.load().lora_norm_rope(
         _dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx,
         _offsets(x, heads, head_dim, x_col_off), ws, eps, y.data_ptr(), ldy,
         _offsets(y, heads, head_dim, y_col_off), positions.data_ptr(), inv_freq.data_ptr(),
-        attn_scale, bool(interleaved), _stream(stream)))
+        attn_scale, bool(interleaved), st))
     return y
 
 
