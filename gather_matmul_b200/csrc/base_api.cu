@@ -150,7 +150,7 @@ lora_status lora_matmul_fp8(lora_dtype dtype, int T, int N, int K, const void* q
   if (s == LORA_OK) s = check_scale(q_scale);
   if (s == LORA_OK) s = check_scale(w_scale);
   if (s != LORA_OK) return s;
-  const MatmulFp8Args a = {q, ldq, q_scale, W, ldw, w_scale, y, ldy, T, N, K};
+  const MatmulFp8Args a = {q, ldq, q_scale, W, ldw, w_scale, y, ldy, T, N, K, 0};
   cudaGetLastError();
   return from_cuda(launch_matmul_fp8(dtype, a, (cudaStream_t)stream));
 }
@@ -177,7 +177,7 @@ lora_status lora_linear_fp8(lora_dtype dtype, int T, int N, int K, const void* x
   if (s != LORA_OK) return s;
   float* scale = reinterpret_cast<float*>(static_cast<char*>(work) + a256((size_t)T * up16(K)));
   const QuantArgs qa = {x, ldx, work, up16(K), scale, T, K, 1};
-  const MatmulFp8Args ma = {work, up16(K), scale, W, ldw, w_scale, y, ldy, T, N, K};
+  const MatmulFp8Args ma = {work, up16(K), scale, W, ldw, w_scale, y, ldy, T, N, K, 1};
   cudaGetLastError();
   cudaError_t e = launch_quantize_fp8(dtype, qa, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_matmul_fp8(dtype, ma, (cudaStream_t)stream);

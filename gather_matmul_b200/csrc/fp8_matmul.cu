@@ -75,6 +75,7 @@ struct WideParams {
   int64_t ldy;
   int T, N, KB, NB, KS;
   int m_tiles, n_tiles;
+  int w_early;                   // W is not written by the previous launch
 };
 
 // Tile order: groups of 8 token tiles, output tiles within a group, so that the
@@ -140,6 +141,19 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   ptx::cluster_wait();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // W's tiles of the first stages before the wait for the previous kernel (the
+  // quantiser of the same call, which writes q and its scales only)
+  const int early = P.w_early && first < n_tiles ? min(kWStages, kb1 - kb0) : 0;
+  if (warp == kWPromote && lane == 0 && early > 0) {
+    int m0, n0;
+    wide_tile(P, first, m0, n0);
+    for (int i = 0; i < early; ++i) {
+      if (half == 0) ptx::mbar_arrive_expect_tx(&full[i], 2 * L::kStage);
+      ptx::tma_load_2d_pair(smem + i * L::kStage + L::kOperand, &P.tmW, (kb0 + i) * kBlockK,
+                            n0 + (int)half * kWHalf, ptx::map_rank(&full[i], leader));
+    }
+  }
+  __syncwarp();
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
 
@@ -159,8 +173,9 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
               break;
             char* st = smem + s * L::kStage;
             const uint32_t bar = bar0 + 8 * s;
-            if (half == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
+            if (half == 0 && it >= early) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
             ptx::tma_load_2d_pair(st, &P.tmQ, kb * kBlockK, m0 + (int)half * kWHalf, bar);
+            if (it < early) continue;
             ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK,
                                   n0 + (int)half * kWHalf, bar);
           }
@@ -397,21 +412,24 @@ constexpr int kNRows = 128;
 constexpr int kNBufs = 4;           // tensor-memory buffers
 constexpr int kNSlots = 4;          // groups of 4 blocks whose scales are in shared memory
 
-template <int TN>
+// Two CTAs per SM of up to 64 tokens, or one with twice the stages (DEEP).
+template <int TN, bool DEEP>
 struct NarrowShape {
   static constexpr int kPromote = TN <= 64 ? 4 : 8;                 // promotion warps
   static constexpr int kCols = TN / (kPromote / 4);                 // columns of each
-  static constexpr int kThreads = 32 * (kPromote + 3);
-  static constexpr int kCtas = TN <= 64 ? 2 : 1;                    // per SM
+  static constexpr int kCtas = DEEP ? 1 : 2;                        // per SM
+  static constexpr int kIssue = TN == 64 && !DEEP ? 1 : 2;          // issuing warps (registers)
+  static constexpr int kThreads = 32 * (kPromote + 2 + kIssue);
   static constexpr int kW = kNRows * kBlockK;
   static constexpr int kStage = kW + TN * kBlockK;
-  static constexpr int kStages = TN == 16 || TN == 128 ? 6 : (TN == 64 ? 4 : 5);
-  static constexpr int kBufs = kNBufs;
-  static constexpr int kTmem = TN * kBufs;
-  static constexpr int kScale = kStages * kStage;                   // per slot [4][TN]
-  static constexpr int kSlot = 4 * 4 * TN;
+  static constexpr int kSlot = 4 * 4 * TN;                          // scales [4][TN]
+  // as many stages as fit beside the scales and barriers (under 1.5 KB)
+  static constexpr int kStages =
+      (227 * 1024 / kCtas - 3584 - kNSlots * kSlot) / kStage;
+  static constexpr int kTmem = TN * kNBufs;
+  static constexpr int kScale = kStages * kStage;
   static constexpr int kBar = kScale + kNSlots * kSlot;
-  static constexpr int kTotal = kBar + 8 * 2 * (kStages + kBufs + kNSlots) + 64 + 1024;
+  static constexpr int kTotal = kBar + 8 * 2 * (kStages + kNBufs + kNSlots) + 64 + 1024;
   static_assert(kCtas * (kTotal + 1024) <= 228 * 1024, "CTAs per SM");
 };
 
@@ -422,13 +440,14 @@ struct NarrowParams {
   uint16_t* y;
   int64_t ldy;
   int T, N, KB, KS, n_tiles;
+  int w_early;              // W is not written by the previous launch
 };
 
-template <typename E, int TN>
-__global__ void __launch_bounds__(NarrowShape<TN>::kThreads, NarrowShape<TN>::kCtas)
+template <typename E, int TN, bool DEEP>
+__global__ void __launch_bounds__(NarrowShape<TN, DEEP>::kThreads, NarrowShape<TN, DEEP>::kCtas)
 matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
-  using L = NarrowShape<TN>;
-  constexpr int kS = L::kStages, kB = L::kBufs, kPW = L::kPromote, kC = L::kCols;
+  using L = NarrowShape<TN, DEEP>;
+  constexpr int kS = L::kStages, kB = kNBufs, kPW = L::kPromote, kC = L::kCols;
   constexpr int kChunk = kC < 32 ? kC : 32;
   constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kNRows, TN);
   extern __shared__ char smem_raw[];
@@ -475,6 +494,15 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // W's tiles of the first stages before the wait for the previous kernel (the
+  // quantiser of the same call, which writes q and its scales only)
+  const int early = P.w_early ? min(kS, nkb) : 0;
+  if (warp == kPW && lane == 0)
+    for (int i = 0; i < early; ++i) {
+      ptx::mbar_arrive_expect_tx(&full[i], L::kStage);
+      ptx::tma_load_2d(smem + i * L::kStage, &P.tmW, (kb0 + i) * kBlockK, n0, &full[i]);
+    }
+  __syncwarp();
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
 
@@ -489,8 +517,10 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
         const int s = i % kS;
         if (i >= kS && !ptx::mbar_wait_asm(em + 8 * s, (i / kS - 1) & 1, stop_at)) break;
         char* st = smem + s * L::kStage;
-        ptx::mbar_arrive_expect_tx(&full[s], L::kStage);
-        ptx::tma_load_2d(st, &P.tmW, (kb0 + i) * kBlockK, n0, &full[s]);
+        if (i >= early) {
+          ptx::mbar_arrive_expect_tx(&full[s], L::kStage);
+          ptx::tma_load_2d(st, &P.tmW, (kb0 + i) * kBlockK, n0, &full[s]);
+        }
         ptx::tma_load_2d(st + L::kW, &P.tmQ, (kb0 + i) * kBlockK, t0, &full[s]);
       }
       // the last stages' release: no signal may arrive after this CTA has left
@@ -498,12 +528,13 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
         if (!ptx::mbar_wait_asm(em + 8 * (i % kS), (i / kS) & 1, stop_at)) break;
     }
     __syncwarp();
-  } else if (warp == kPW + 1) {
-    // the whole warp runs the loop, an elected thread issues
+  } else if (warp == kPW + 1 || warp == kPW + 3) {
+    // two issuing warps take the blocks in turn (one waits while the other
+    // issues); the whole warp runs the loop, an elected thread the instructions
     const bool one = ptx::elect_one();
     const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty);
     const uint64_t dw = ptx::umma_desc_kmajor(ptx::smem_u32(smem), 128);
-    for (int i = 0; i < nkb; ++i) {
+    for (int i = warp == kPW + 1 ? 0 : 1; i < nkb; i += L::kIssue) {
       const int s = i % kS, b = i % kB;
       bool ok = ptx::mbar_wait_asm(te + 8 * b, (i / kB + 1) & 1, stop_at);
       ok &= ptx::mbar_wait_asm(fu + 8 * s, (i / kS) & 1, stop_at);
@@ -701,6 +732,7 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
   P.T = a.T;
   P.N = a.N;
   P.KB = (a.K + kBlockK - 1) / kBlockK;
+  P.w_early = a.w_early;
   P.NB = (a.N + kBlockK - 1) / kBlockK;
   P.m_tiles = (a.T + kWTile - 1) / kWTile;
   P.n_tiles = (a.N + kWTile - 1) / kWTile;
@@ -717,7 +749,7 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
                                                    WideSmem::kTotal, st);
 }
 
-template <typename E, int TN>
+template <typename E, int TN, bool DEEP>
 cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
   NarrowParams P;
   memset(&P, 0, sizeof(P));
@@ -731,6 +763,7 @@ cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
   P.T = a.T;
   P.N = a.N;
   P.KB = (a.K + kBlockK - 1) / kBlockK;
+  P.w_early = a.w_early;
   P.n_tiles = (a.N + kNRows - 1) / kNRows;
   const int units = P.n_tiles * ((a.T + TN - 1) / TN);
   int KS = 1;
@@ -738,12 +771,12 @@ cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
   // The first split pays for the exchange only if it fills idle SMs or shortens
   // a long K: 12.8 us unsplit against 14.1 in two at 48 x 8192 x 4096 (128 CTAs),
   // but 18.8 in two against 20.9 at 256 x 2048 x 8192.
-  const int room = NarrowShape<TN>::kCtas * sm_count();
+  const int room = NarrowShape<TN, DEEP>::kCtas * sm_count();
   if (units * 2 <= sm_count() || P.KB >= 48)
     while (KS < 8 && units * KS * 2 <= room && P.KB >= 4 * KS) KS *= 2;
   P.KS = KS;
-  return cluster_launch<matmul_fp8_narrow_kernel<E, TN>>(
-      P, units * KS, KS, NarrowShape<TN>::kThreads, NarrowShape<TN>::kTotal, st);
+  return cluster_launch<matmul_fp8_narrow_kernel<E, TN, DEEP>>(
+      P, units * KS, KS, NarrowShape<TN, DEEP>::kThreads, NarrowShape<TN, DEEP>::kTotal, st);
 }
 
 template <typename E>
@@ -759,19 +792,20 @@ cudaError_t matmul_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st
   //   256 x 8192             29.8  26.2   20.2   19.9
   //   256 x 14336            54.0  50.2   39.4   21.7
   //   512 x 4096 x 14336           76.0   52.6   37.5
-  // Tiles of 32 tokens are the best while two CTAs per SM hold them all, 128
-  // while one does; past that only the wide kernel's reuse of both operands
-  // keeps up.  Few tiles of a long K go to the wide kernel, whose two parts of
-  // K then fill the device.
+  // Tiles of 32 tokens are the best while one CTA per SM holds them all, then 64
+  // with one deep CTA per SM (15.4 at 256 x 4096), then 32 with two, 128 with one;
+  // past that only the wide kernel's reuse of both operands keeps up.  Few tiles
+  // of a long K go to the wide kernel, whose two parts of K then fill the device.
   const int sms = sm_count(), n = (a.N + kNRows - 1) / kNRows;
   const auto units = [&](int tn) { return (int64_t)n * ((a.T + tn - 1) / tn); };
   const int64_t tiles = (int64_t)((a.N + kWTile - 1) / kWTile) * ((a.T + kWTile - 1) / kWTile);
-  if (a.T <= 16) return narrow_launch<E, 16>(a, st);
-  if (a.T <= 32 || units(32) <= sms) return narrow_launch<E, 32>(a, st);
+  if (a.T <= 16) return narrow_launch<E, 16, false>(a, st);
+  if (a.T <= 32 || units(32) <= sms) return narrow_launch<E, 32, false>(a, st);
   if (a.T > 128 && 4 * tiles <= sms && a.K >= 40 * kBlockK) return wide_launch<E>(dt, a, st);
-  if (units(32) <= 2 * sms) return narrow_launch<E, 32>(a, st);
-  if (a.T <= 64) return narrow_launch<E, 64>(a, st);
-  if (a.T <= 128 || units(128) <= sms) return narrow_launch<E, 128>(a, st);
+  if (units(64) <= sms) return narrow_launch<E, 64, true>(a, st);
+  if (units(32) <= 2 * sms) return narrow_launch<E, 32, false>(a, st);
+  if (a.T <= 64) return narrow_launch<E, 64, false>(a, st);
+  if (a.T <= 128 || units(128) <= sms) return narrow_launch<E, 128, true>(a, st);
   return wide_launch<E>(dt, a, st);
 }
 

@@ -85,6 +85,10 @@ struct MatmulFp8Args {
   void* y;
   int64_t ldy;
   int T, N, K;
+  // 1: the previous launch on the stream is this call's quantiser, which lets
+  // its successor start only once everything before it has finished, and writes
+  // q and q_scale only: W may be read before that launch has finished
+  int w_early;
 };
 
 struct RopeArgs {
