@@ -32,7 +32,8 @@ def sources():
 
 def deps():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "lora.h")]
+        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
+        [os.path.join(INCLUDE, "lora.h"), os.path.abspath(__file__)]
 
 
 def stale(out=LIB):

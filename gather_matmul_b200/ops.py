@@ -22,6 +22,7 @@ index in [0, S) means no LoRA work at all, so nothing is enqueued.  Without a
 host copy the call runs, and the kernels skip tokens without an adapter.
 """
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -400,7 +401,10 @@ def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor
     return torch.tensor(list(out), dtype=torch.float64, device=device), attn.value
 
 
-def _offsets(t, heads, dim, col_off):
+@functools.lru_cache(maxsize=256)
+def _layout(heads, dim, col_off):
+    """(heads, first columns, past-the-end column) of a tuple of slices, as the
+    C call takes them; a pure function of its arguments."""
     if col_off is None:
         col_off, c = [], 0
         for h in heads:
@@ -408,22 +412,31 @@ def _offsets(t, heads, dim, col_off):
             c += h * dim
     if len(col_off) != len(heads):
         raise ValueError("one column offset per slice")
-    for h, c in zip(heads, col_off):
-        if c + h * dim > t.shape[1]:
-            raise ValueError("a slice's heads reach past the last column")
-    return (ctypes.c_int64 * len(heads))(*col_off)
+    end = max([c + h * dim for h, c in zip(heads, col_off)], default=0)
+    return ((ctypes.c_int32 * len(heads))(*heads), (ctypes.c_int64 * len(heads))(*col_off), end)
 
 
-def _rope_common(x, y, heads, positions, inv_freq):
+def _offsets(t, heads, dim, col_off):
+    h, off, end = _layout(tuple(heads), dim, None if col_off is None else tuple(col_off))
+    if end > t.shape[1]:
+        raise ValueError("a slice's heads reach past the last column")
+    return h, off
+
+
+def _rope_args(x, y, heads, head_dim, positions, inv_freq, x_col_off, y_col_off):
     ldx, ldy = _rows(x, "x"), _rows(y, "y", x.dtype)
     T = x.shape[0]
     if y.shape[0] != T:
         raise ValueError("x and y must have the same rows")
-    if positions.dtype != torch.int64 or not positions.is_contiguous() or positions.numel() != T:
+    if positions.dtype is not torch.int64 or not positions.is_contiguous() or \
+            positions.numel() != T:
         raise TypeError("positions must be a contiguous int64 tensor of one position per token")
-    if inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+    if inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a contiguous float64 tensor of one frequency per pair")
-    return T, ldx, ldy, (ctypes.c_int32 * len(heads))(*heads)
+    h, xo = _offsets(x, heads, head_dim, x_col_off)
+    _, yo = _offsets(y, heads, head_dim, y_col_off)
+    head = (_dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx, xo)
+    return head, (y.data_ptr(), ldy, yo, positions.data_ptr(), inv_freq.data_ptr())
 
 
 def rope(x: torch.Tensor, y: torch.Tensor, heads: Sequence[int], head_dim: int,
@@ -436,13 +449,9 @@ def rope(x: torch.Tensor, y: torch.Tensor, heads: Sequence[int], head_dim: int,
     halves or interleaved; the rest are copied.  y may be x with the same
     offsets (in place).  positions: int64 [T]; inv_freq, attn_scale from
     rope_frequencies()."""
-    T, ldx, ldy, h = _rope_common(x, y, heads, positions, inv_freq)
+    head, tail = _rope_args(x, y, heads, head_dim, positions, inv_freq, x_col_off, y_col_off)
     st = _here(stream, x, y, positions, inv_freq)
-    _check("lora_rope", _lib.load().lora_rope(
-        _dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx,
-        _offsets(x, heads, head_dim, x_col_off), y.data_ptr(), ldy,
-        _offsets(y, heads, head_dim, y_col_off), positions.data_ptr(), inv_freq.data_ptr(),
-        attn_scale, bool(interleaved), st))
+    _check("lora_rope", _lib.load().lora_rope(*head, *tail, attn_scale, bool(interleaved), st))
     return y
 
 
@@ -453,20 +462,17 @@ def norm_rope(x: torch.Tensor, weights, y: torch.Tensor, heads: Sequence[int], h
     """rope() with a root-mean-square norm of each head before it, in one
     pass: weights holds one tensor [head_dim] of x's dtype per slice, or None
     for a slice without a norm."""
-    T, ldx, ldy, h = _rope_common(x, y, heads, positions, inv_freq)
+    head, tail = _rope_args(x, y, heads, head_dim, positions, inv_freq, x_col_off, y_col_off)
     if len(weights) != len(heads):
         raise ValueError("one weight (or None) per slice")
-    for w in weights:
-        if w is not None and (w.dtype != x.dtype or not w.is_contiguous() or
-                              w.numel() != head_dim):
+    given = [w for w in weights if w is not None]
+    for w in given:
+        if w.dtype is not x.dtype or not w.is_contiguous() or w.numel() != head_dim:
             raise TypeError("a weight must be a contiguous tensor of head_dim elements of x's dtype")
-    st = _here(stream, x, y, positions, inv_freq, *[w for w in weights if w is not None])
+    st = _here(stream, x, y, positions, inv_freq, *given)
     ws = (ctypes.c_void_p * len(weights))(*[None if w is None else w.data_ptr() for w in weights])
     _check("lora_norm_rope", _lib.load().lora_norm_rope(
-        _dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx,
-        _offsets(x, heads, head_dim, x_col_off), ws, eps, y.data_ptr(), ldy,
-        _offsets(y, heads, head_dim, y_col_off), positions.data_ptr(), inv_freq.data_ptr(),
-        attn_scale, bool(interleaved), st))
+        *head, ws, eps, *tail, attn_scale, bool(interleaved), st))
     return y
 
 

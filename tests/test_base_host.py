@@ -220,7 +220,9 @@ def test_slices_past_the_last_column_are_refused():
         ops._offsets(x, [4], 64, None)
     with pytest.raises(ValueError, match="past the last column"):
         ops._offsets(x, [1], 64, [192])
-    assert list(ops._offsets(x, [1, 2], 64, None)) == [0, 64]
+    assert list(ops._offsets(x, [1, 2], 64, None)[1]) == [0, 64]
+    with pytest.raises(ValueError, match="one column offset"):
+        ops._offsets(x, [1, 2], 64, [0])
 
 
 # ---------------------------------------------------------------- the quantiser's rounding
