@@ -66,8 +66,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 14336 against 77.1 with a scalar product and the rounding in integer steps.
 __device__ __forceinline__ uint32_t scaled2(float x0, float x1, uint64_t r2) {
   const uint64_t k64 = 0x4280000042800000ull, km64 = 0xc2800000c2800000ull;   // 64, -64
-  uint64_t t;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(ptx::pack2(x0, x1)), "l"(r2));
+  const uint64_t t = ptx::fmul2(ptx::pack2(x0, x1), r2);
   const uint64_t h = ptx::ffma2(t, km64, ptx::ffma2(t, k64, t));
   return __nv_cvt_float2_to_fp8x2(make_float2(ptx::lo32(h), ptx::hi32(h)), __NV_SATFINITE,
                                   __NV_E4M3);
@@ -107,7 +106,7 @@ __device__ __forceinline__ void store8(uint8_t* row, int c, int K, const uint4& 
 // following rows; each half-warp takes G groups, cw apart, whose loads are all
 // in flight at once and whose divisions G lanes make together.
 template <typename E, int G>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, 6)
 quant_rows_kernel(const E* x, int64_t ldx, uint8_t* q, int64_t ldq, float* scale, int T, int K,
                   int KB, int cw) {
   ptx::grid_dep_wait();
@@ -197,7 +196,8 @@ cudaError_t quant_launch(const QuantArgs& a, cudaStream_t st) {
                                              a.scale, a.T, a.K, KB));
   }
   // four groups per half-warp once there are enough to fill the device (71.6 us
-  // against 93 with one at 8192 x 14336; one token of 4096: 2.1 us against 1.6)
+  // against 93 with one at 8192 x 14336, 67.8 with six CTAs per SM; one token of
+  // 4096: 2.1 us against 1.6)
   const int G = KB >= 4 && (int64_t)a.T * KB >= 32768 ? 4 : 1;
   int cw = 1;
   while (cw < kQGroups && cw * G < KB) cw *= 2;

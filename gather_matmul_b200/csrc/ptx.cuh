@@ -254,6 +254,11 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // acc += s2 * {lo, hi}: the pair is named inside the instruction's own block, so
 // that adjacent registers (a tensor-memory load's) are used where they are.
 __device__ __forceinline__ void ffma2_acc(uint64_t& acc, uint64_t s2, uint32_t lo, uint32_t hi) {

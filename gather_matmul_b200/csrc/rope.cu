@@ -8,8 +8,9 @@
 // per token for all its heads, into shared memory, while its loads of the
 // heads are in flight.
 //
-// Bound: memory (2 bytes read and 2 written per element; 30 us at 8192 tokens of
-// 32 + 8 heads of 128, 5.6 TB/s).  A group of L lanes holds one head: each lane
+// Bound: memory (2 bytes read and 2 written per element; 27.9 us at 8192 tokens
+// of 32 + 8 heads of 128, 6.0 TB/s), with norms nearly as much by the issue of
+// instructions (36.0 us; packed fp32 arithmetic needed more registers: 42.6).  A group of L lanes holds one head: each lane
 // the two vectors of V elements that its pairs join, so a half-split rotation
 // needs no exchange between lanes, and the norm needs one sum over the L lanes.
 // The order of the table decides much: with (cos, sin) pairs in the order of the
@@ -56,7 +57,10 @@ __device__ __forceinline__ typename Vec<V>::type pack(const float* f) {
   return v;
 }
 
-constexpr int kRThreads = 512;   // most threads of a CTA
+// Most threads of a CTA, and the CTAs per SM that the registers are held to.
+// 27.9 us (36.0 with norms) at 8192 tokens of 32 + 8 heads of 128, against 29.9
+// (38.2) with up to 512 threads, 30.4 (42.5) with up to 128.
+constexpr int kRThreads = 256, kRCtas = 5;
 
 struct RopeGrid {
   int L;            // lanes per head, a power of two up to 32
@@ -68,7 +72,7 @@ struct RopeGrid {
 // dim / 2 / V; the first rot / 2 / V of them are rotated.  TPT consecutive
 // tokens per thread, all of whose loads are in flight at once.
 template <typename E, int V, int ITEMS, int TPT, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kRThreads) rope_kernel(const RopeArgs a, const RopeGrid G) {
+__global__ void __launch_bounds__(kRThreads, kRCtas) rope_kernel(const RopeArgs a, const RopeGrid G) {
   typedef typename Vec<V>::type vec;
   extern __shared__ float4 cs4[];         // [slots * TPT][rot]
   float* cs = reinterpret_cast<float*>(cs4);
@@ -245,8 +249,8 @@ cudaError_t rope_tokens(const RopeArgs& a, bool norm, cudaStream_t st) {
                        : rope_launch<E, V, ITEMS, TPT, false>(a, norm, st);
 }
 
-// Two tokens per thread once that leaves several CTAs per SM (about 320 threads
-// each): 30.0 us against 33.8 at 8192 tokens of 40 heads of 128 (38.1 against
+// Two tokens per thread once that leaves several CTAs per SM.  With CTAs of 320
+// threads: 30.0 us against 33.8 at 8192 tokens of 40 heads of 128 (38.1 against
 // 47.2 with norms; four tokens 31.0 and 38.8), 3.6 against 3.3 at 512 tokens.
 template <typename E, int V, int ITEMS>
 cudaError_t rope_layout(const RopeArgs& a, bool norm, cudaStream_t st) {
