@@ -410,6 +410,7 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
 // ---------------------------------------------------------------------------
 constexpr int kNRows = 128;
 constexpr int kNBufs = 4;           // tensor-memory buffers
+constexpr int kLongK = 48;          // blocks: a K that two parts shorten enough
 constexpr int kNSlots = 4;          // groups of 4 blocks whose scales are in shared memory
 
 // Two CTAs per SM of up to 64 tokens, or one with twice the stages (DEEP).
@@ -449,6 +450,7 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
   using L = NarrowShape<TN, DEEP>;
   constexpr int kS = L::kStages, kB = kNBufs, kPW = L::kPromote, kC = L::kCols;
   constexpr int kChunk = kC < 32 ? kC : 32;
+  constexpr bool kAhead = DEEP && TN <= 64;
   constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kNRows, TN);
   extern __shared__ char smem_raw[];
   char* smem = align1024(smem_raw);
@@ -593,6 +595,14 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
       for (int j = 0; j < n; ++j, sc += 4 * TN) {
         const int b = (kb + j) % kB;
         const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc);
+        // With registers to spare the scales are read before the block's sums are
+        // awaited, behind the wait's own latency: 10.4 us against 11.2 at 128 x
+        // 4096 x 4096 (elsewhere it spills: 43 us against 40 with 128 tokens).
+        ulonglong2 sv[kAhead ? kC / 4 : 1];
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int i = 0; i < kC / 4; ++i) sv[i] = s2[i];
+        }
         ok &= ptx::mbar_wait_asm(tf + 8 * b, ((kb + j) / kB) & 1, stop_at);
         __syncwarp();
         ptx::tc_fence_after();
@@ -614,10 +624,10 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
           }
 #pragma unroll
           for (int i = 0; i < kChunk / 4; ++i) {
-            const ulonglong2 v = s2[c * (kChunk / 4) + i];
-            uint64_t* a = acc + c * (kChunk / 2) + 2 * i;
-            ptx::ffma2_acc(a[0], v.x, r[4 * i], r[4 * i + 1]);
-            ptx::ffma2_acc(a[1], v.y, r[4 * i + 2], r[4 * i + 3]);
+            const int at = c * (kChunk / 4) + i;
+            const ulonglong2 v = kAhead ? sv[kAhead ? at : 0] : s2[at];
+            ptx::ffma2_acc(acc[2 * at], v.x, r[4 * i], r[4 * i + 1]);
+            ptx::ffma2_acc(acc[2 * at + 1], v.y, r[4 * i + 2], r[4 * i + 3]);
           }
         }
       }
@@ -630,7 +640,7 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
     }
   }
   const int n = n0 + row;
-  if (KS == 1) {
+  if (DEEP || KS == 1) {
     if (warp < kPW && n < P.N) {
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
@@ -640,7 +650,7 @@ matmul_fp8_narrow_kernel(const __grid_constant__ NarrowParams P) {
               Elem<E>::from_f32(j & 1 ? ptx::hi32(acc[j / 2]) : ptx::lo32(acc[j / 2]));
       }
     }
-  } else {
+  } else if constexpr (!DEEP) {
     // part p of K hands every other part its share of the tokens (TN / KS),
     // through the drained stages; each adds the KS shares in rank order
     const int sh = __ffs(TN) - __ffs(KS), share = 1 << sh;   // TN / KS; both powers of two
@@ -766,14 +776,19 @@ cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
   P.w_early = a.w_early;
   P.n_tiles = (a.N + kNRows - 1) / kNRows;
   const int units = P.n_tiles * ((a.T + TN - 1) / TN);
+  // Parts of K.  Few CTAs are split in 8 or 4 (K = 4096, us: 4 x 1024, 8 CTAs, 7.4
+  // in 2, 5.3 in 4, 4.3 in 8; 64 x 4096, 64 CTAs, 11.7 in 1, 10.7 in 2, 9.4 in 4;
+  // but 1 x 4096, 32 CTAs, 6.2 in 4, 6.8 in 8), a short K only as far as one CTA
+  // per SM (77 x 1504 x 1008, 60 CTAs, 4.2 in 1, 5.3 in 4).  Two parts hardly
+  // repay the exchange: only of a long K (256 x 2048 x 8192: 18.8, 20.9 in 1).
+  // Deep CTAs are chosen where they fill the device unsplit.
+  const int sms = sm_count();
   int KS = 1;
-  // K split until the CTAs fill the device, two blocks at least for each part.
-  // The first split pays for the exchange only if it fills idle SMs or shortens
-  // a long K: 12.8 us unsplit against 14.1 in two at 48 x 8192 x 4096 (128 CTAs),
-  // but 18.8 in two against 20.9 at 256 x 2048 x 8192.
-  const int room = NarrowShape<TN, DEEP>::kCtas * sm_count();
-  if (units * 2 <= sm_count() || P.KB >= 48)
-    while (KS < 8 && units * KS * 2 <= room && P.KB >= 4 * KS) KS *= 2;
+  if constexpr (!DEEP) {
+    if (P.KB >= 8 && 8 * units <= sms) KS = 8;
+    else if (P.KB >= 4 && 4 * units <= (P.KB >= 16 ? 2 * sms : sms)) KS = 4;
+    else if (P.KB >= kLongK && units <= sms) KS = 2;
+  }
   P.KS = KS;
   return cluster_launch<matmul_fp8_narrow_kernel<E, TN, DEEP>>(
       P, units * KS, KS, NarrowShape<TN, DEEP>::kThreads, NarrowShape<TN, DEEP>::kTotal, st);
@@ -784,23 +799,29 @@ cudaError_t matmul_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st
   // The tile by how many CTAs it makes.  Measured (us, K = 4096 unless given):
   //   T x N           16     32     64    128    256 (wide)
   //   1 x 4096        6.9    7.3    9.0   12     33
-  //   64 x 8192      13.9   12.8   18.2   18.2   50
+  //   64 x 8192      13.9   12.5   18.2   18.2   50
   //   64 x 28672     62.6   36.4   27.7   36.4   67
-  //   128 x 4096     13.9   12.6   15.2   13.7   18
+  //   128 x 4096     11.9   11.7   14.9   13.5   18
   //   128 x 28672   114     67.9   50.8   40.0   51
   //   256 x 4096             15.8  18.4   18.9   18.2
   //   256 x 8192             29.8  26.2   20.2   19.9
   //   256 x 14336            54.0  50.2   39.4   21.7
   //   512 x 4096 x 14336           76.0   52.6   37.5
-  // Tiles of 32 tokens are the best while one CTA per SM holds them all, then 64
-  // with one deep CTA per SM (15.4 at 256 x 4096), then 32 with two, 128 with one;
-  // past that only the wide kernel's reuse of both operands keeps up.  Few tiles
+  // Tiles of 32 tokens are the best while one CTA per SM holds them all (in deep
+  // CTAs, unless K is split: 10.4 at 128 x 4096, 11.8 at 64 x 8192), then 64 with
+  // one deep CTA per SM (15.2 at 256 x 4096), then 32 with two, 128 with one; past
+  // that only the wide kernel's reuse of both operands keeps up.  Few tiles
   // of a long K go to the wide kernel, whose two parts of K then fill the device.
+  // 16 tokens also where they leave CTAs to spare: 5.7 against 6.2 at 64 x 1024,
+  // 4.0 against 4.5 at 128 x 1024 x 1024.
   const int sms = sm_count(), n = (a.N + kNRows - 1) / kNRows;
   const auto units = [&](int tn) { return (int64_t)n * ((a.T + tn - 1) / tn); };
   const int64_t tiles = (int64_t)((a.N + kWTile - 1) / kWTile) * ((a.T + kWTile - 1) / kWTile);
-  if (a.T <= 16) return narrow_launch<E, 16, false>(a, st);
-  if (a.T <= 32 || units(32) <= sms) return narrow_launch<E, 32, false>(a, st);
+  const int KB = (a.K + kBlockK - 1) / kBlockK;
+  if (a.T <= 16 || units(16) * (KB >= 16 ? 4 : 1) <= sms) return narrow_launch<E, 16, false>(a, st);
+  if (a.T <= 32 || 2 * units(32) <= sms) return narrow_launch<E, 32, false>(a, st);
+  if (units(32) <= sms)
+    return KB < kLongK ? narrow_launch<E, 32, true>(a, st) : narrow_launch<E, 32, false>(a, st);
   if (a.T > 128 && 4 * tiles <= sms && a.K >= 40 * kBlockK) return wide_launch<E>(dt, a, st);
   if (units(64) <= sms) return narrow_launch<E, 64, true>(a, st);
   if (units(32) <= 2 * sms) return narrow_launch<E, 32, false>(a, st);
