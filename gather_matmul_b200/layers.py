@@ -42,12 +42,15 @@ class AttentionInputs:
         widths = [q_heads * head_dim, kv_heads * head_dim, kv_heads * head_dim]
         if W.shape[0] != sum(widths) or [b.shape[1] for b in B] != widths:
             raise ValueError("W's rows and B's stacks must be the q, k and v heads")
+        S, r, K = A[0].shape
+        if K != W.shape[1] or any(a.shape != A[0].shape for a in A) or \
+                any(b.shape[0] != S or b.shape[2] != r for b in B):
+            raise ValueError("A must be [S, r, K] stacks for W's K columns, B [S, width, r]")
         self.W, self.w_scale, self.A, self.B = W, w_scale, list(A), list(B)
         self.heads, self.head_dim = [q_heads, kv_heads], head_dim
         self.inv_freq, self.attn_scale, self.interleaved = inv_freq, attn_scale, interleaved
         self.norms = None if q_norm is None and k_norm is None else [q_norm, k_norm]
         self.eps, self.scale, self.max_tokens = eps, scale, max_tokens
-        S, r, K = A[0].shape
         self.work = ops.linear_fp8_workspace(max_tokens, K, W.device)
         self.meta = ops.workspace(max_tokens, S, W.device)
         self.buf = torch.empty(len(A) * max_tokens * r, dtype=torch.float32, device=W.device)

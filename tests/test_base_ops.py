@@ -440,6 +440,62 @@ def test_calls_on_another_stream_and_in_a_graph():
     assert torch.equal(got, out) and not torch.equal(got, want)
 
 
+@pytest.mark.parametrize("T", [3, 100, 300, 700])
+def test_linear_sees_what_was_written_just_before(T):
+    """The product reads its first weight tiles before the quantiser of the same
+    call has ended: weights, inputs and outputs that change from call to call
+    on one stream, without a wait between, must still be each call's own."""
+    N, K = 640, 1024
+    g = gen(41)
+    wides = [(0.05 * torch.randn(N, K, generator=g, device="cuda")).to(BF16) for _ in range(4)]
+    xs = [torch.randn(T, K, generator=g, device="cuda").to(BF16) for _ in range(4)]
+    W, ws = torch.empty(N, K, dtype=FP8, device="cuda"), torch.empty(N // 128, K // 128, device="cuda")
+    x, y = torch.empty(T, K, dtype=BF16, device="cuda"), torch.empty(T, N, dtype=BF16, device="cuda")
+    work = ops.linear_fp8_workspace(T, K)
+
+    def call(i, wait):
+        ops.quantize_fp8(wides[i], W, ws, block_rows=128)
+        if wait:
+            torch.cuda.synchronize()
+        ops.linear_fp8(xs[i], W, ws, y, work)
+        if wait:
+            torch.cuda.synchronize()
+    want = []
+    for i in range(4):
+        call(i, True)
+        want.append(y.clone())
+    got = []
+    for j in range(24):
+        call(j % 4, False)
+        got.append(y.clone())
+    x.copy_(xs[2])
+    ops.linear_fp8(x, W, ws, y, work)          # behind a torch kernel that wrote x
+    x.fill_(float("nan"))                      # and before one that overwrites it
+    torch.cuda.synchronize()
+    for j, v in enumerate(got):
+        assert torch.equal(v, want[j % 4]), j
+    ops.linear_fp8(xs[2], W, ws, got[0], work)
+    assert torch.equal(y, got[0])
+
+
+def test_two_streams_with_a_workspace_each():
+    T, N, K = 200, 768, 2048
+    g = gen(51)
+    x = [torch.randn(T, K, generator=g, device="cuda").to(F16) for _ in range(2)]
+    q, qs, W, ws, _, _ = make(T, N, K, F16, 52)
+    work = [ops.linear_fp8_workspace(T, K) for _ in range(2)]
+    want = [ops.linear_fp8(x[i], W, ws, torch.empty(T, N, dtype=F16, device="cuda"), work[i]) for i in range(2)]
+    out = [torch.empty(T, N, dtype=F16, device="cuda") for _ in range(2)]
+    st = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(st[i]):
+                ops.linear_fp8(x[i], W, ws, out[i], work[i])
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("norms", [True, False], ids=["norms", "plain"])
 @pytest.mark.parametrize("T", [1, 9, 130])
@@ -523,6 +579,15 @@ def test_attention_inputs_refusals():
     layer = AttentionInputs(W, ws, A, B, 2, 1, 64, f, max_tokens=8)
     with pytest.raises(ValueError):
         AttentionInputs(W, ws, A, B, 1, 1, 64, f, max_tokens=8)
+    with pytest.raises(ValueError):
+        AttentionInputs(W, ws, [A[0][:, :, :64].contiguous()], B, 2, 1, 64, f, max_tokens=8)   # another K
+    with pytest.raises(ValueError):
+        AttentionInputs(W, ws, A, [b[:1].contiguous() for b in B], 2, 1, 64, f, max_tokens=8)  # another S
+    none = torch.empty(0, 128, dtype=BF16, device="cuda")
+    before = ops.launch_count()
+    layer(none, torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"),
+          torch.empty(0, 256, dtype=BF16, device="cuda"))
+    assert ops.launch_count() == before
     x = torch.zeros(9, 128, dtype=BF16, device="cuda")
     with pytest.raises(ValueError):
         layer(x, torch.zeros(9, dtype=torch.int32, device="cuda"), torch.zeros(9, dtype=torch.int64, device="cuda"),
