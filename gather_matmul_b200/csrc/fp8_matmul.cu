@@ -49,7 +49,7 @@ __device__ __forceinline__ void drain_copies() {
 constexpr int kWTile = 256;                 // tokens and outputs per pair
 constexpr int kWHalf = 128;                 // rows of A and of B that one CTA loads
 constexpr int kWStages = 5;
-constexpr int kWBufs = 2;                   // tensor-memory buffers of 256 columns
+constexpr int kWBufs = 4;                   // tensor-memory buffers of 128 columns
 constexpr int kWPromote = 8;                // promotion warps
 constexpr int kWSlots = 4;                  // groups of 4 blocks whose scales are in shared memory
 constexpr int kWThreads = 32 * (kWPromote + 4);
@@ -59,8 +59,8 @@ constexpr int kWRegsPromote = 232, kWRegsRest = 40;
 struct WideSmem {
   static constexpr int kOperand = kWHalf * kBlockK;             // 16 KB
   static constexpr int kStage = 2 * kOperand;
-  static constexpr int kOut = kWStages * kStage;                // 4 KB per promotion warp
-  static constexpr int kScale = kOut + kWPromote * 4096;        // per slot: 4 of 128 tokens, 4 of 2 of W
+  static constexpr int kOut = kWStages * kStage;                // 3 x 2 KB per promotion warp
+  static constexpr int kScale = kOut + kWPromote * 6144;        // per slot: 4 of 128 tokens, 4 of 2 of W
   static constexpr int kSlot = 16 * (kWHalf + 2);
   static constexpr int kBar = kScale + kWSlots * kSlot;
   static constexpr int kTotal = kBar + 8 * 2 * (kWStages + kWBufs + kWSlots) + 64 + 1024;
@@ -68,7 +68,7 @@ struct WideSmem {
 static_assert(WideSmem::kTotal <= 227 * 1024, "one CTA per SM");
 
 struct WideParams {
-  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128} bytes; y {64, 32} elements
+  CUtensorMap tmQ, tmW, tmY;     // boxes {128, 128}, {128, 64} bytes; y {32, 32} elements
   const float* q_scale;
   const float* w_scale;
   uint16_t* y;
@@ -92,7 +92,7 @@ template <typename E>
 __global__ void __launch_bounds__(kWThreads, 1)
 matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   using L = WideSmem;
-  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWTile);
+  constexpr uint32_t kIdesc = ptx::umma_idesc_e4m3(kWTile, kWHalf);
   extern __shared__ char smem_raw[];
   char* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -115,11 +115,11 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
   if (tid == 0) {
     for (int s = 0; s < kWStages; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
+      ptx::mbar_init(&empty[s], 2);             // both issuing warps
     }
     for (int b = 0; b < kWBufs; ++b) {
       ptx::mbar_init(&tfull[b], 1);
-      ptx::mbar_init(&tempty[b], 2 * kWPromote);
+      ptx::mbar_init(&tempty[b], kWPromote);    // half of them, in both CTAs
     }
     for (int s = 0; s < kWSlots; ++s) {
       ptx::mbar_init(&sfull[s], 32);
@@ -149,8 +149,10 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
     wide_tile(P, first, m0, n0);
     for (int i = 0; i < early; ++i) {
       if (half == 0) ptx::mbar_arrive_expect_tx(&full[i], 2 * L::kStage);
-      ptx::tma_load_2d_pair(smem + i * L::kStage + L::kOperand, &P.tmW, (kb0 + i) * kBlockK,
-                            n0 + (int)half * kWHalf, ptx::map_rank(&full[i], leader));
+      for (int h = 0; h < 2; ++h)
+        ptx::tma_load_2d_pair(smem + i * L::kStage + L::kOperand + h * 64 * kBlockK, &P.tmW,
+                              (kb0 + i) * kBlockK, n0 + h * kWHalf + (int)half * 64,
+                              ptx::map_rank(&full[i], leader));
     }
   }
   __syncwarp();
@@ -176,8 +178,11 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
             if (half == 0 && it >= early) ptx::mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
             ptx::tma_load_2d_pair(st, &P.tmQ, kb * kBlockK, m0 + (int)half * kWHalf, bar);
             if (it < early) continue;
-            ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK,
-                                  n0 + (int)half * kWHalf, bar);
+            // W's rows in two boxes of 64: the MMA of output half h takes rows
+            // h * 64 .. of either CTA, which then are h * 128 + half * 64 .. of the tile
+            ptx::tma_load_2d_pair(st + L::kOperand, &P.tmW, kb * kBlockK, n0 + (int)half * 64, bar);
+            ptx::tma_load_2d_pair(st + L::kOperand + 64 * kBlockK, &P.tmW, kb * kBlockK,
+                                  n0 + kWHalf + (int)half * 64, bar);
           }
         }
         // the last stages' release: no signal may arrive after this CTA has left
@@ -222,30 +227,32 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (half == 0) {
-      // the pair's even CTA issues: two warps take the blocks in turn, each with
-      // one of the two buffers, so that one waits while the other's MMAs run; the
-      // whole warp runs the loop, an elected thread the instructions
-      const int b = warp == kWPromote + 1 ? 0 : 1;
+      // the pair's even CTA issues, one warp for each 128-column half of the tile:
+      // a half's buffer goes to its four promotion warps and back without waiting
+      // for the other half (66.4 us against 69.4 at 2048 x 8192 x 4096 with MMAs of
+      // 256 columns); the whole warp runs the loop, an elected thread the
+      // instructions
+      const int h = warp == kWPromote + 1 ? 0 : 1;
       const bool one = ptx::elect_one();
-      const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty + b);
+      const uint32_t fu = ptx::smem_u32(full), te = ptx::smem_u32(tempty + h);
       const uint64_t dq = ptx::umma_desc_kmajor(ptx::smem_u32(smem), 128);
-      const uint64_t dw = dq + (L::kOperand >> 4);
+      const uint64_t dw = dq + ((L::kOperand + h * 64 * kBlockK) >> 4);
       const uint16_t mask = (uint16_t)(3u << leader);
       const int total = ((n_tiles - first + stride - 1) / stride) * (kb1 - kb0);
-      for (int it = b; it < total; it += 2) {
-        const int s = it % kWStages;
+      for (int it = 0; it < total; ++it) {
+        const int s = it % kWStages, b = it & 1;
         bool ok = ptx::mbar_wait_asm(fu + 8 * s, (it / kWStages) & 1, stop_at);
-        ok &= ptx::mbar_wait_asm(te, (it / 2 + 1) & 1, stop_at);
+        ok &= ptx::mbar_wait_asm(te + 16 * b, (it / 2 + 1) & 1, stop_at);
         if (!__all_sync(~0u, ok)) break;
         ptx::tc_fence_after();
         if (one) {
-          const uint32_t d = tmem + b * kWTile;
+          const uint32_t d = tmem + (2 * b + h) * kWHalf;
           const uint64_t qa = dq + (uint32_t)(s * (L::kStage >> 4));
           const uint64_t wa = dw + (uint32_t)(s * (L::kStage >> 4));
 #pragma unroll
           for (int k = 0; k < kBlockK / 32; ++k)
             ptx::tc_mma_f8_pair(d, qa + k * 2, wa + k * 2, kIdesc, k > 0);
-          ptx::tc_commit_pair(&tfull[b], mask);
+          ptx::tc_commit_pair(&tfull[2 * b + h], mask);
           ptx::tc_commit_pair(&empty[s], mask);
         }
         __syncwarp();
@@ -258,95 +265,125 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
     // of W) per four warps
     const int quad = warp & 3, wh = warp >> 2, col = wh * kWHalf, row = quad * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + col;
-    const uint32_t te = ptx::map_rank(&tempty[0], leader);
-    const uint32_t tf = ptx::smem_u32(tfull), sf = ptx::smem_u32(sfull);
-    char* out = smem + L::kOut + warp * 4096;
-    int it = 0, g = 0;
+    const uint32_t te = ptx::map_rank(&tempty[wh], leader);
+    const uint32_t tf = ptx::smem_u32(tfull + wh), sf = ptx::smem_u32(sfull);
+    char* out = smem + L::kOut + warp * 6144;
+    const int nkb = kb1 - kb0, groups = (nkb + 3) / 4;
+    const int all_groups = (n_tiles - first + stride - 1) / stride * groups;
+    int it = 0, g = 0, box = 0;
+    bool ok = true;
+    // A group's scales (4 blocks) are read while the group before is worked on:
+    // a wait and a read here take 300 clocks beside the copies and the MMAs.
+    float4 q4, w4;
+    const auto scales = [&](int group, uint32_t ready) {
+      const int sl = group % kWSlots;
+      ok &= ptx::mbar_wait_asm(sf + 8 * sl, (group / kWSlots) & 1, stop_at, ready);
+      const float4* sc = reinterpret_cast<const float4*>(smem + L::kScale + sl * L::kSlot);
+      q4 = sc[row];
+      w4 = sc[kWHalf + wh];
+    };
+    if (all_groups > 0) scales(0, 0);
     for (int tile = first; tile < n_tiles; tile += stride) {
+      uint64_t acc[2][32];
+      // 32 columns at a time: the next ones are on their way from tensor memory
+      // while the sums of these are formed
+      uint32_t r0[32], r1[32];
+      ok &= ptx::mbar_wait_asm(tf + 16 * (it & 1), (it / 2) & 1, stop_at);
+      __syncwarp();
+      ptx::tc_fence_after();
+      ptx::tc_ld32(trow + (it & 1) * kWTile, r0);
+      float4 s4;
+      uint32_t sready = 0;
+      bool loaded = true;
+      const auto block = [&](auto start, int j) {
+        const auto add = [&](uint64_t* sums, uint64_t s2, const uint32_t* r) {
+          if constexpr (decltype(start)::value) ptx::fmul2_set16(sums, s2, r);
+          else ptx::ffma2_acc16(sums, s2, r);
+        };
+        if ((j & 3) == 0) {
+          s4 = make_float4(q4.x * w4.x, q4.y * w4.y, q4.z * w4.z, q4.w * w4.w);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sempty[g % kWSlots]);
+          ++g;
+          loaded = g >= all_groups;
+          sready = loaded ? 0 : ptx::mbar_test(sf + 8 * (g % kWSlots), (g / kWSlots) & 1);
+        }
+        const int b = it & 1;
+        const uint32_t t0 = trow + b * kWTile;
+        const uint64_t s2 = ptx::pack2(s4.x, s4.x);
+        s4.x = s4.y; s4.y = s4.z; s4.z = s4.w;
+        const bool more = j + 1 < nkb;
+        ptx::tc_wait_ld32(r0);
+        ptx::tc_ld32(t0 + 32, r1);
+        add(acc[0], s2, r0);
+        ptx::tc_wait_ld32(r1);
+        ptx::tc_ld32(t0 + 64, r0);
+        add(acc[0] + 16, s2, r1);
+        ptx::tc_wait_ld32(r0);
+        const uint32_t ready = ptx::mbar_test(tf + 16 * (b ^ 1), ((it + 1) / 2) & 1);
+        ptx::tc_ld32(t0 + 96, r1);
+        add(acc[1], s2, r0);
+        ptx::tc_wait_ld32(r1);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(te + 16 * b);
+        if (!loaded) {
+          scales(g, sready);
+          loaded = true;
+        }
+        if (more) {
+          ok &= ptx::mbar_wait_asm(tf + 16 * (b ^ 1), ((it + 1) / 2) & 1, stop_at, ready);
+          __syncwarp();
+          ptx::tc_fence_after();
+          ptx::tc_ld32(trow + (b ^ 1) * kWTile, r0);
+        }
+        add(acc[1] + 16, s2, r1);
+        ++it;
+      };
+      block(std::true_type{}, 0);
+      for (int j = 1; j < nkb; ++j) block(std::false_type{}, j);
       int m0, n0;
       wide_tile(P, tile, m0, n0);
       m0 += (int)half * kWHalf;
       const int t = m0 + row;
-      uint64_t acc[2][32];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i / 32][i % 32] = 0;
-      // 32 columns at a time: the next ones are on their way from tensor memory
-      // while the sums of these are formed
-      uint32_t r0[32], r1[32];
-      bool ok = ptx::mbar_wait_asm(tf + 8 * (it & 1), (it / 2) & 1, stop_at);
-      __syncwarp();
-      ptx::tc_fence_after();
-      ptx::tc_ld32(trow + (it & 1) * kWTile, r0);
-      for (int kb = kb0; kb < kb1; kb += 4, ++g) {
-        const int sl = g % kWSlots, n = min(4, kb1 - kb);
-        ok &= ptx::mbar_wait_asm(sf + 8 * sl, (g / kWSlots) & 1, stop_at);
-        const float4* sc = reinterpret_cast<const float4*>(smem + L::kScale + sl * L::kSlot);
-        const float4 q4 = sc[row];
-        float4 s4 = sc[kWHalf + wh];
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sempty[sl]);
-        s4.x *= q4.x; s4.y *= q4.y; s4.z *= q4.z; s4.w *= q4.w;
-        for (int j = 0; j < n; ++j, ++it) {
-          const int b = it & 1;
-          const uint32_t t0 = trow + b * kWTile;
-          const uint64_t s2 = ptx::pack2(s4.x, s4.x);
-          s4.x = s4.y; s4.y = s4.z; s4.z = s4.w;
-          ptx::tc_wait_ld32(r0);
-          ptx::tc_ld32(t0 + 32, r1);
-          ptx::ffma2_acc16(acc[0], s2, r0);
-          ptx::tc_wait_ld32(r1);
-          ptx::tc_ld32(t0 + 64, r0);
-          ptx::ffma2_acc16(acc[0] + 16, s2, r1);
-          ptx::tc_wait_ld32(r0);
-          const bool more = kb + j + 1 < kb1;
-          const uint32_t ready = ptx::mbar_test(tf + 8 * (b ^ 1), ((it + 1) / 2) & 1);
-          ptx::tc_ld32(t0 + 96, r1);
-          ptx::ffma2_acc16(acc[1], s2, r0);
-          ptx::tc_wait_ld32(r1);
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(te + 8 * b);
-          if (more) {
-            ok &= ptx::mbar_wait_asm(tf + 8 * (b ^ 1), ((it + 1) / 2) & 1, stop_at, ready);
-            __syncwarp();
-            ptx::tc_fence_after();
-            ptx::tc_ld32(trow + (b ^ 1) * kWTile, r0);
-          }
-          ptx::ffma2_acc16(acc[1] + 16, s2, r1);
-        }
-      }
       if (!ok) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i / 32][i % 32] = 0x7fffffff7fffffffull;
       }
       if (KS == 1) {
-        // 32 rows x 64 columns at a time through shared memory, in the 128-byte
-        // swizzle the tensor map expects, and out by TMA.  TMA clips at T, but in
-        // a row only at whole 16 bytes: the map ends at N rounded down to 8, and
-        // the last columns are stored one by one
+        // 32 rows x 32 columns at a time through a ring of three boxes in shared
+        // memory, in the 64-byte swizzle the tensor map expects, and out by TMA.
+        // TMA clips at T, but in a row only at whole 16 bytes: the map ends at N
+        // rounded down to 8, and the last columns are stored one by one
         const int n8 = P.N & ~7;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (lane == 0) ptx::bulk_wait_read_all();   // the copy before has left
+        for (int h = 0; h < 4; ++h) {
+          if (lane == 0) ptx::bulk_wait_read<2>();    // the copy three boxes ago has left
           __syncwarp();
-          char* o = out + lane * 128;
+          char* o = out + box * 2048;
+          char* mine = o + lane * 64;
+          box = box == 2 ? 0 : box + 1;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             uint4 v;
             uint32_t* w = &v.x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = Elem<E>::pack2(ptx::lo32(acc[h][j * 4 + i]), ptx::hi32(acc[h][j * 4 + i]));
-            *reinterpret_cast<uint4*>(o + ((j ^ (lane & 7)) << 4)) = v;
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t u = acc[h / 2][(h % 2) * 16 + j * 4 + i];
+              w[i] = Elem<E>::pack2(ptx::lo32(u), ptx::hi32(u));
+            }
+            *reinterpret_cast<uint4*>(mine + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          const int mr = m0 + quad * 32, nc = n0 + col + h * 64;
-          if (lane == 0 && mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, out);
-          if (lane == 0) ptx::bulk_commit();
-          if (n8 >= nc && n8 < nc + 64 && t < P.T) {
+          const int mr = m0 + quad * 32, nc = n0 + col + h * 32;
+          if (lane == 0) {
+            if (mr < P.T && nc < n8) ptx::tma_store_2d(&P.tmY, nc, mr, o);
+            ptx::bulk_commit();
+          }
+          if (n8 >= nc && n8 < nc + 32 && t < P.T) {
             const uint16_t* v =
-                reinterpret_cast<const uint16_t*>(o + ((((n8 - nc) >> 3) ^ (lane & 7)) << 4));
+                reinterpret_cast<const uint16_t*>(mine + ((((n8 - nc) >> 3) ^ ((lane >> 1) & 3)) << 4));
             for (int n = n8; n < P.N; ++n) P.y[(int64_t)t * P.ldy + n] = v[n - n8];
           }
         }
@@ -731,9 +768,9 @@ cudaError_t wide_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) 
   WideParams P;
   memset(&P, 0, sizeof(P));
   cudaError_t e = encode_tmap_2d_bytes(&P.tmQ, a.q, a.K, a.T, a.ldq, kBlockK, kWHalf, 128);
-  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, kWHalf, 128);
+  if (e == cudaSuccess) e = encode_tmap_2d_bytes(&P.tmW, a.W, a.K, a.N, a.ldw, kBlockK, 64, 128);
   if (e == cudaSuccess) e = encode_tmap_2d(&P.tmY, dt, a.y, a.N < 8 ? 8 : a.N & ~7, a.T,
-                                           (uint64_t)a.ldy * 2, 64, 32, 128);
+                                           (uint64_t)a.ldy * 2, 32, 32, 64);
   if (e != cudaSuccess) return e;
   P.q_scale = a.q_scale;
   P.w_scale = a.w_scale;

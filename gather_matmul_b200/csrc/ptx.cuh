@@ -152,6 +152,11 @@ __device__ __forceinline__ void bulk_wait_all() {
 __device__ __forceinline__ void bulk_wait_read_all() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
+// Until at most N of this thread's bulk groups still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 // 2-D tiled tensor copy global -> shared (no multicast).
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
@@ -287,6 +292,29 @@ __device__ __forceinline__ void ffma2_acc16(uint64_t* acc, uint64_t s2, const ui
       " mov.b64 t, {%47, %48};\n fma.rn.f32x2 %15, %16, t, %15;\n"
      "}"
       : "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7]), "+l"(acc[8]), "+l"(acc[9]), "+l"(acc[10]), "+l"(acc[11]), "+l"(acc[12]), "+l"(acc[13]), "+l"(acc[14]), "+l"(acc[15])
+      : "l"(s2), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]));
+}
+// the same without the sums so far: acc[i] = s2 * {r[2i], r[2i+1]}
+__device__ __forceinline__ void fmul2_set16(uint64_t* acc, uint64_t s2, const uint32_t* r) {
+  asm volatile("{\n .reg .b64 t;\n"
+      " mov.b64 t, {%17, %18};\n mul.rn.f32x2 %0, %16, t;\n"
+      " mov.b64 t, {%19, %20};\n mul.rn.f32x2 %1, %16, t;\n"
+      " mov.b64 t, {%21, %22};\n mul.rn.f32x2 %2, %16, t;\n"
+      " mov.b64 t, {%23, %24};\n mul.rn.f32x2 %3, %16, t;\n"
+      " mov.b64 t, {%25, %26};\n mul.rn.f32x2 %4, %16, t;\n"
+      " mov.b64 t, {%27, %28};\n mul.rn.f32x2 %5, %16, t;\n"
+      " mov.b64 t, {%29, %30};\n mul.rn.f32x2 %6, %16, t;\n"
+      " mov.b64 t, {%31, %32};\n mul.rn.f32x2 %7, %16, t;\n"
+      " mov.b64 t, {%33, %34};\n mul.rn.f32x2 %8, %16, t;\n"
+      " mov.b64 t, {%35, %36};\n mul.rn.f32x2 %9, %16, t;\n"
+      " mov.b64 t, {%37, %38};\n mul.rn.f32x2 %10, %16, t;\n"
+      " mov.b64 t, {%39, %40};\n mul.rn.f32x2 %11, %16, t;\n"
+      " mov.b64 t, {%41, %42};\n mul.rn.f32x2 %12, %16, t;\n"
+      " mov.b64 t, {%43, %44};\n mul.rn.f32x2 %13, %16, t;\n"
+      " mov.b64 t, {%45, %46};\n mul.rn.f32x2 %14, %16, t;\n"
+      " mov.b64 t, {%47, %48};\n mul.rn.f32x2 %15, %16, t;\n"
+     "}"
+      : "=&l"(acc[0]), "=&l"(acc[1]), "=&l"(acc[2]), "=&l"(acc[3]), "=&l"(acc[4]), "=&l"(acc[5]), "=&l"(acc[6]), "=&l"(acc[7]), "=&l"(acc[8]), "=&l"(acc[9]), "=&l"(acc[10]), "=&l"(acc[11]), "=&l"(acc[12]), "=&l"(acc[13]), "=&l"(acc[14]), "=&l"(acc[15])
       : "l"(s2), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]));
 }
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
