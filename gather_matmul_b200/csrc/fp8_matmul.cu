@@ -9,13 +9,9 @@
 // its scale, to fp32 sums in registers ("promotion") while the tensor core
 // works on the next block in another buffer.
 //
-// Two kernels:
-//   wide    256 tokens x 256 outputs per pair of CTAs (cta_group::2), tokens on
-//           the MMA's M side.  Bound by the tensor core and the promotion.
-//   narrow  128 outputs x 16..128 tokens per CTA, weights on the M side, K split
-//           over a cluster.  Bound by reading the weights once.
+// Two kernels, wide for many tokens and narrow for few (below).
 //
-// A wait that runs out (a second; never in a sound run) ends the kernel and
+// A wait that runs out (up to a second; never in a sound run) ends the kernel and
 // makes its outputs NaN.
 #include <string.h>
 
@@ -44,7 +40,19 @@ __device__ __forceinline__ void drain_copies() {
 }
 
 // ---------------------------------------------------------------------------
-// Wide: a pair of CTAs per 256 x 256 tile
+// Wide: 256 tokens x 256 outputs per pair of CTAs (cta_group::2), tokens on the
+// MMA's M side, so that a thread's tensor-memory lane is one token and a block's
+// scale one number per thread and half of the tile.
+//
+// 256 x 256 is the largest tile whose fp32 sums fit the registers (128 a thread in
+// eight warps of each CTA), and reads the fewest operand bytes per MMA: 64 KB per
+// block of 512 MMA clocks and pair.  Tensor memory then holds two blocks.
+//
+// What bounds it: the hand-over MMA -> promotion -> MMA, two blocks deep, whose
+// steps take 150 to 200 clocks each beside the copies; the tensor pipe is busy 56 %
+// of the time.  At 8192 x 28672 x 4096: 792 to 830 us (2.3 to 2.4 PFLOP/s) at full
+// clocks, 938 us in a long run, which stands at the power limit at 1.49 GHz.
+// Without the promotion's arithmetic: 750; without the MMAs: 508.
 // ---------------------------------------------------------------------------
 constexpr int kWTile = 256;                 // tokens and outputs per pair
 constexpr int kWHalf = 128;                 // rows of A and of B that one CTA loads
@@ -445,7 +453,15 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
 }
 
 // ---------------------------------------------------------------------------
-// Narrow: 128 outputs x TN tokens per CTA, K split over a cluster
+// Narrow: 128 outputs x TN tokens per CTA, weights on the M side (a full M at any
+// number of tokens), K split over a cluster where the tiles leave SMs idle.  A
+// thread's lane is one output, its columns are tokens: the tokens' scales, times
+// the tile's one scale of W, come through shared memory.
+//
+// What bounds it: one or a few tokens, reading W (12.7 us for 58.7 MB at 1 x 4096 x
+// 14336, 4.6 TB/s); up to 256 tokens, the hand-over of each block between copies,
+// MMA and promotion, 0.2 us with 32 tokens (10.4 us at 128 x 4096 x 4096) and
+// 0.35 with 64 (15.0 us at 256 x 4096 x 4096), which CTAs beside each other hide.
 // ---------------------------------------------------------------------------
 constexpr int kNRows = 128;
 constexpr int kNBufs = 4;           // tensor-memory buffers
