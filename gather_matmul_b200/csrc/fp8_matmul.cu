@@ -460,8 +460,8 @@ matmul_fp8_wide_kernel(const __grid_constant__ WideParams P) {
 //
 // What bounds it: one or a few tokens, reading W (12.7 us for 58.7 MB at 1 x 4096 x
 // 14336, 4.6 TB/s); up to 256 tokens, the hand-over of each block between copies,
-// MMA and promotion, 0.2 us with 32 tokens (10.4 us at 128 x 4096 x 4096) and
-// 0.35 with 64 (15.0 us at 256 x 4096 x 4096), which CTAs beside each other hide.
+// MMA and promotion, 0.2 us with 32 tokens (10.0 us at 128 x 4096 x 4096) and
+// 0.3 with 64 (13.3 us at 256 x 4096 x 4096), which CTAs beside each other hide.
 // ---------------------------------------------------------------------------
 constexpr int kNRows = 128;
 constexpr int kNBufs = 4;           // tensor-memory buffers
@@ -471,7 +471,9 @@ constexpr int kNSlots = 4;          // groups of 4 blocks whose scales are in sh
 // Two CTAs per SM of up to 64 tokens, or one with twice the stages (DEEP).
 template <int TN, bool DEEP>
 struct NarrowShape {
-  static constexpr int kPromote = TN <= 64 ? 4 : 8;                 // promotion warps
+  // promotion warps, as many as registers allow: 13.3 us with 16, 13.5 with 8, 15.1
+  // with 4 at 256 x 4096 x 4096 (64 tokens, deep)
+  static constexpr int kPromote = TN == 16 || (TN == 64 && !DEEP) ? 4 : (TN == 32 ? 8 : 16);
   static constexpr int kCols = TN / (kPromote / 4);                 // columns of each
   static constexpr int kCtas = DEEP ? 1 : 2;                        // per SM
   static constexpr int kIssue = TN == 64 && !DEEP ? 1 : 2;          // issuing warps (registers)
@@ -857,14 +859,14 @@ cudaError_t matmul_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st
   //   64 x 8192      13.9   12.5   18.2   18.2   50
   //   64 x 28672     62.6   36.4   27.7   36.4   67
   //   128 x 4096     11.9   11.7   14.9   13.5   18
-  //   128 x 28672   114     67.9   50.8   40.0   51
+  //   128 x 28672   114     67.9   50.8   37.7   51
   //   256 x 4096             15.8  18.4   18.9   18.2
   //   256 x 8192             29.8  26.2   20.2   19.9
   //   256 x 14336            54.0  50.2   39.4   21.7
   //   512 x 4096 x 14336           76.0   52.6   37.5
   // Tiles of 32 tokens are the best while one CTA per SM holds them all (in deep
-  // CTAs, unless K is split: 10.4 at 128 x 4096, 11.8 at 64 x 8192), then 64 with
-  // one deep CTA per SM (15.2 at 256 x 4096), then 32 with two, 128 with one; past
+  // CTAs, unless K is split: 10.0 at 128 x 4096, 10.6 at 64 x 8192), then 64 with
+  // one deep CTA per SM (13.3 at 256 x 4096), then 32 with two, 128 with one; past
   // that only the wide kernel's reuse of both operands keeps up.  Few tiles
   // of a long K go to the wide kernel, whose two parts of K then fill the device.
   // 16 tokens also where they leave CTAs to spare: 5.7 against 6.2 at 64 x 1024,
