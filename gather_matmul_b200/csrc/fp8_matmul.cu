@@ -853,20 +853,24 @@ cudaError_t narrow_launch(const MatmulFp8Args& a, cudaStream_t st) {
 
 template <typename E>
 cudaError_t matmul_launch(lora_dtype dt, const MatmulFp8Args& a, cudaStream_t st) {
-  // The tile by how many CTAs it makes.  Measured (us, K = 4096 unless given):
+  // The tile by how many CTAs it makes.  Measured (us, K = 4096 unless given,
+  // the better of a tile's two depths):
   //   T x N           16     32     64    128    256 (wide)
-  //   1 x 4096        6.9    7.3    9.0   12     33
-  //   64 x 8192      13.9   12.5   18.2   18.2   50
-  //   64 x 28672     62.6   36.4   27.7   36.4   67
-  //   128 x 4096     11.9   11.7   14.9   13.5   18
-  //   128 x 28672   114     67.9   50.8   37.7   51
-  //   256 x 4096             15.8  18.4   18.9   18.2
-  //   256 x 8192             29.8  26.2   20.2   19.9
-  //   256 x 14336            54.0  50.2   39.4   21.7
-  //   512 x 4096 x 14336           76.0   52.6   37.5
+  //   1 x 4096        6.3    6.9    8.3   15     25
+  //   64 x 8192      12.7   10.7   12.6   17.4   31
+  //   64 x 28672     60.3   35.7   25.8   35.1   68
+  //   128 x 4096     12.3   10.1   12.3   18.4   21
+  //   128 x 14336    43.4   29.1   25.2   20.3   31
+  //   128 x 28672   109     66.2   47.8   37.9   49
+  //   256 x 4096     23.1   15.6   13.4   18.8   17.1
+  //   256 x 8192     44.0   29.3   24.7   19.9   19.3
+  //   160 x 8192            23.9          19.5   25.3
+  //   256 x 14336    75.4   50.4   47.0   37.4   19.5
+  //   512 x 4096 x 14336    82.6   65.9   50.8   34.7
   // Tiles of 32 tokens are the best while one CTA per SM holds them all (in deep
   // CTAs, unless K is split: 10.0 at 128 x 4096, 10.6 at 64 x 8192), then 64 with
-  // one deep CTA per SM (13.3 at 256 x 4096), then 32 with two, 128 with one; past
+  // one deep CTA per SM (13.3 at 256 x 4096), then 32 with two, 128 with one (the wide
+  // kernel is level there with full tiles only); past
   // that only the wide kernel's reuse of both operands keeps up.  Few tiles
   // of a long K go to the wide kernel, whose two parts of K then fill the device.
   // 16 tokens also where they leave CTAs to spare: 5.7 against 6.2 at 64 x 1024,
