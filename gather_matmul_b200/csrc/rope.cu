@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(kRThreads, kRCtas) rope_kernel(const RopeArgs 
             // pairs lie inside each vector: V / 2 in va, V / 2 in vb
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-              
               const float a0 = fa[i][2 * j], a1 = fa[i][2 * j + 1];
               const float b0 = fb[i][2 * j], b1 = fb[i][2 * j + 1];
               fa[i][2 * j] = a0 * co[j] - a1 * si[j];
@@ -204,7 +203,6 @@ __global__ void __launch_bounds__(kRThreads, kRCtas) rope_kernel(const RopeArgs 
           } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-              
               const float u0 = fa[i][j], u1 = fb[i][j];
               fa[i][j] = u0 * co[j] - u1 * si[j];
               fb[i][j] = u1 * co[j] + u0 * si[j];
