@@ -95,7 +95,8 @@ lora_status rope_impl(lora_dtype dtype, int T, int dim, int rot, int n_slices,
       const char* xj = static_cast<const char*>(x) + 2 * x_col_off[j];
       const char* yj = static_cast<const char*>(y) + 2 * y_col_off[j];
       const int64_t wj = 2 * (int64_t)heads[j] * dim;
-      const bool in_place = i == j && yi == xj && ldx == ldy;
+      // a single row has no next one, so its strides need not agree
+      const bool in_place = i == j && yi == xj && (ldx == ldy || T == 1);
       if (!in_place && share(yi, wi, 2 * ldy, xj, wj, 2 * ldx, T)) return LORA_ERR_INVALID_ARG;
       if (j < i && share(yi, wi, 2 * ldy, yj, wj, 2 * ldy, T)) return LORA_ERR_INVALID_ARG;
     }

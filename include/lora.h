@@ -486,9 +486,10 @@ LORA_API lora_status lora_rope_frequencies(int rot, double base, lora_rope_kind 
  *   heads       host int32 [n_slices], heads of each slice, side by side from
  *               column x_col_off[i] of x (and y_col_off[i] of y).
  *   x, y        device [T, ldx], [T, ldy] dtype.  y may be x with ldy = ldx
- *               and equal offsets (in place); otherwise the slices read and
- *               written must not share memory (checked).  Columns of y
- *               outside the slices are left as they were.
+ *               (of one row: any strides) and equal offsets (in place);
+ *               otherwise the slices read and written must not share memory
+ *               (checked).  Columns of y outside the slices are left as they
+ *               were.
  *   positions   device int64 [T], of any sign; |position| < 2^53.
  *   inv_freq    device fp64 [rot / 2], 8-byte aligned.
  * head_dim a multiple of 8 up to LORA_MAX_HEAD_DIM, rot even, 2 .. head_dim;
