@@ -287,6 +287,16 @@ def shrink_noalloc(x: torch.Tensor, A: Sequence[torch.Tensor], idx: torch.Tensor
 # ---------------------------------------------------------------------------
 _FP8 = torch.float8_e4m3fn
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The C calls take sizes as int, and ctypes cuts a larger number down to its
+# low 32 bits without a word: such numbers are refused here.
+_INT_MAX = 0x7fffffff
+
+
+def _int(call, v):
+    v = int(v)
+    if not -_INT_MAX <= v <= _INT_MAX:
+        raise LoraError(call, _lib.LORA_ERR_UNSUPPORTED)
+    return v
 
 
 def _here(stream, *tensors):
@@ -309,6 +319,8 @@ def _rows(t, name, dtype=None):
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0):
         raise ValueError(f"{name} must be 2-D with unit column stride")
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+        raise ValueError(f"{name} must have less than 2^31 rows and columns")
     # a single row has no next one: any stride that the alignment rules take
     return stride[0] if shape[0] > 1 else -(-max(shape[1], 1) // 16) * 16
 
@@ -330,6 +342,8 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_ro
     T, K = x.shape
     if q.shape != x.shape:
         raise ValueError("q must have the shape of x")
+    if block_rows != 1:
+        block_rows = _int("lora_quantize_fp8", block_rows)
     _scales(scale, "scale", -(-T // block_rows) if block_rows > 0 else 0, K)
     st = _here(stream, x, q, scale)
     _check("lora_quantize_fp8", _lib.load().lora_quantize_fp8(
@@ -358,9 +372,10 @@ def matmul_fp8(q: torch.Tensor, q_scale: torch.Tensor, W: torch.Tensor, w_scale:
 
 def linear_fp8_workspace(T: int, K: int, device="cuda") -> torch.Tensor:
     """A workspace for linear_fp8() of up to T tokens of K columns."""
-    n = _lib.load().lora_linear_fp8_workspace_bytes(int(T), int(K))
+    call = "lora_linear_fp8_workspace_bytes"
+    n = _lib.load().lora_linear_fp8_workspace_bytes(_int(call, T), _int(call, K))
     if n == 0:
-        raise LoraError("lora_linear_fp8_workspace_bytes", _lib.LORA_ERR_UNSUPPORTED)
+        raise LoraError(call, _lib.LORA_ERR_UNSUPPORTED)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -393,10 +408,11 @@ def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor
     "linear", "ntk", "yarn" or "bands" (see lora_rope_frequencies)."""
     if kind not in _lib.ROPE_KINDS:
         raise ValueError(f"kind must be one of {sorted(_lib.ROPE_KINDS)}")
-    out = (ctypes.c_double * max(int(rot) // 2, 1))()
+    rot = _int("lora_rope_frequencies", rot)
+    out = (ctypes.c_double * max(min(rot, _lib.LORA_MAX_HEAD_DIM) // 2, 1))()
     attn = ctypes.c_float()
     _check("lora_rope_frequencies", _lib.load().lora_rope_frequencies(
-        int(rot), float(base), _lib.ROPE_KINDS[kind], float(factor), float(original_length),
+        rot, float(base), _lib.ROPE_KINDS[kind], float(factor), float(original_length),
         float(beta_fast), float(beta_slow), out, ctypes.byref(attn)))
     return torch.tensor(list(out), dtype=torch.float64, device=device), attn.value
 
@@ -412,6 +428,8 @@ def _layout(heads, dim, col_off):
             c += h * dim
     if len(col_off) != len(heads):
         raise ValueError("one column offset per slice")
+    if dim <= 0 or any(h <= 0 for h in heads) or any(c < 0 for c in col_off):
+        raise LoraError("lora_rope", _lib.LORA_ERR_INVALID_ARG)
     end = max([c + h * dim for h, c in zip(heads, col_off)], default=0)
     return ((ctypes.c_int32 * len(heads))(*heads), (ctypes.c_int64 * len(heads))(*col_off), end)
 
@@ -433,9 +451,12 @@ def _rope_args(x, y, heads, head_dim, positions, inv_freq, x_col_off, y_col_off)
         raise TypeError("positions must be a contiguous int64 tensor of one position per token")
     if inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a contiguous float64 tensor of one frequency per pair")
+    rot = 2 * inv_freq.numel()
+    if rot > _INT_MAX:
+        raise LoraError("lora_rope", _lib.LORA_ERR_INVALID_ARG)
     h, xo = _offsets(x, heads, head_dim, x_col_off)
     _, yo = _offsets(y, heads, head_dim, y_col_off)
-    head = (_dtype(x), T, head_dim, 2 * inv_freq.numel(), len(h), h, x.data_ptr(), ldx, xo)
+    head = (_dtype(x), T, head_dim, rot, len(h), h, x.data_ptr(), ldx, xo)
     return head, (y.data_ptr(), ldy, yo, positions.data_ptr(), inv_freq.data_ptr())
 
 
