@@ -23,7 +23,7 @@ class AttentionInputs:
                  block_rows=128); the N columns of y are the q heads, the k
                  heads, then the v heads.
     A, B         LoRA stacks of the q, k and v slices, as for ops.bgmv (A may be
-                 one shared stack).
+                 one shared stack), contiguous and of x's dtype.
     inv_freq, attn_scale   from ops.rope_frequencies.
     q_norm, k_norm         [head_dim] weights of the head norms; both None for a
                            layer without them.
@@ -46,6 +46,13 @@ class AttentionInputs:
         if K != W.shape[1] or any(a.shape != A[0].shape for a in A) or \
                 any(b.shape[0] != S or b.shape[2] != r for b in B):
             raise ValueError("A must be [S, r, K] stacks for W's K columns, B [S, width, r]")
+        if len(A) not in (1, len(B)):
+            raise ValueError("A must hold one stack per slice, or one shared stack")
+        # the kernels take the stacks by address alone
+        if any(t.dtype is not A[0].dtype for t in (*A, *B)):
+            raise TypeError("A and B must be of one dtype, that of x")
+        if not all(t.is_contiguous() and t.device == W.device for t in (*A, *B)):
+            raise ValueError("A and B must be contiguous and on W's device")
         self.W, self.w_scale, self.A, self.B = W, w_scale, list(A), list(B)
         self.heads, self.head_dim = [q_heads, kv_heads], head_dim
         self.inv_freq, self.attn_scale, self.interleaved = inv_freq, attn_scale, interleaved
@@ -62,6 +69,10 @@ class AttentionInputs:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens; the workspaces hold {self.max_tokens}")
+        if x.dtype is not self.A[0].dtype:
+            raise TypeError(f"x must be {self.A[0].dtype}, as the LoRA stacks are")
+        if idx.device != self.W.device:
+            raise ValueError("idx must be on W's device")
         ops.linear_fp8(x, self.W, self.w_scale, y, self.work)
         r = self.A[0].shape[1]
         buf = self.buf[:len(self.A) * T * r].view(len(self.A), T, r)
