@@ -2,15 +2,16 @@
 //   n = x w / sqrt(mean(x^2) + eps),   (a, b) -> m (a cos - b sin, b cos + a sin)
 // at the angle positions[t] * inv_freq[i].
 //
-// The angle is formed in turns in fp64 and reduced to [-1/2, 1/2] there (a
-// position of 2^20 and a frequency of 1 leave fp32 no bits below 2^-4 of a
-// radian); sine and cosine are then taken in fp32.  Each CTA does that once
-// per token for all its heads, into shared memory, while its loads of the
-// heads are in flight.
+// The angle is formed in turns in fp64, with what the products round off carried
+// along, and reduced to about [-1/2, 1/2] there (a position of 2^20 and a
+// frequency of 1 leave fp32 no bits below 2^-4 of a radian; plain fp64 is off by
+// 2e-8 turns at 2^30 and by 0.2 at 2^53); sine and cosine are then taken in fp32.
+// Each CTA does that once per token for all its heads, into shared memory, while
+// its loads of the heads are in flight.
 //
-// Bound: memory (2 bytes read and 2 written per element; 27.9 us at 8192 tokens
+// Bound: memory (2 bytes read and 2 written per element; 28.1 us at 8192 tokens
 // of 32 + 8 heads of 128, 6.0 TB/s), with norms nearly as much by the issue of
-// instructions (36.0 us; packed fp32 arithmetic needed more registers: 42.6).  A group of L lanes holds one head: each lane
+// instructions (36.4 us; packed fp32 arithmetic needed more registers: 42.6).  A group of L lanes holds one head: each lane
 // the two vectors of V elements that its pairs join, so a half-split rotation
 // needs no exchange between lanes, and the norm needs one sum over the L lanes.
 // The order of the table decides much: with (cos, sin) pairs in the order of the
@@ -57,10 +58,32 @@ __device__ __forceinline__ typename Vec<V>::type pack(const float* f) {
   return v;
 }
 
-// Most threads of a CTA, and the CTAs per SM that the registers are held to.
-// 27.9 us (36.0 with norms) at 8192 tokens of 32 + 8 heads of 128, against 29.9
-// (38.2) with up to 512 threads, 30.4 (42.5) with up to 128.
-constexpr int kRThreads = 256, kRCtas = 5;
+// Most threads of a CTA: with 512 the rotation took 29.9 us (38.2 with norms) at
+// 8192 tokens of 32 + 8 heads of 128, with 128 30.4 (42.5).
+constexpr int kRThreads = 256;
+
+// The registers of a thread, as CTAs per SM of so many threads.  Without norms 48,
+// in which the two-token kernels spill 12 to 32 bytes (8 elements to a vector; up
+// to 96 with single elements): 28.1 us at 8192 tokens of 40 heads of 128.  64 leave
+// 27.8 there, but 32.3 against 29.3 at 2048 tokens of 72 heads of 80.  With norms
+// 64, which spill next to nothing: 3.5 us at 512 tokens (4.0 with 48); two tokens
+// with 8 elements to a vector 56 (4 to 36 bytes spilled): 36.4 us at 8192 tokens,
+// 37.3 with 64, 38.1 with 48.
+constexpr int rope_threads(int V, int TPT, bool norm) {
+  return norm && V == 8 && TPT == 2 ? 288 : kRThreads;
+}
+constexpr int rope_ctas(bool norm) { return norm ? 4 : 5; }
+
+// position * f / (2 pi) less a whole number near it.  g + gl are the turns per
+// position to a part in 2^104, and position * g - n is rounded once, as a whole:
+// |position| < 2^53 and f up to 1 leave the result within 5/8 and off by 2^-52 at
+// most (of its own size, in the usual positions).
+__device__ __forceinline__ float turn(int64_t position, double f) {
+  constexpr double kInv = 0x1.45f306dc9c883p-3, kRest = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+  const double x = (double)position, g = f * kInv, gl = fma(f, kRest, fma(f, kInv, -g));
+  const double n = rint(x * g);
+  return (float)fma(x, gl, fma(x, g, -n));
+}
 
 struct RopeGrid {
   int L;            // lanes per head, a power of two up to 32
@@ -72,7 +95,8 @@ struct RopeGrid {
 // dim / 2 / V; the first rot / 2 / V of them are rotated.  TPT consecutive
 // tokens per thread, all of whose loads are in flight at once.
 template <typename E, int V, int ITEMS, int TPT, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kRThreads, kRCtas) rope_kernel(const RopeArgs a, const RopeGrid G) {
+__global__ void __launch_bounds__(rope_threads(V, TPT, NORM), rope_ctas(NORM))
+    rope_kernel(const RopeArgs a, const RopeGrid G) {
   typedef typename Vec<V>::type vec;
   extern __shared__ float4 cs4[];         // [slots * TPT][rot]
   float* cs = reinterpret_cast<float*>(cs4);
@@ -144,9 +168,8 @@ __global__ void __launch_bounds__(kRThreads, kRCtas) rope_kernel(const RopeArgs 
   for (int i = threadIdx.x; i < G.slots * TPT * h; i += blockDim.x) {
     const int64_t tt = first + i / h;
     if (tt >= a.T) break;
-    const double turns = (double)a.positions[tt] * (a.inv_freq[i % h] * 0.15915494309189533577);
     float sn, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &sn, &c);
+    sincospif(2.f * turn(a.positions[tt], a.inv_freq[i % h]), &sn, &c);
     put(cs + (i / h) * a.rot, i % h, c * a.attn_scale, sn * a.attn_scale);
   }
   __syncthreads();

@@ -480,8 +480,10 @@ LORA_API lora_status lora_rope_frequencies(int rot, double base, lora_rope_kind 
  *
  *   attn_scale * (a cos - b sin),  attn_scale * (b cos + a sin)
  *
- * at the angle positions[t] * inv_freq[i] (formed and reduced in fp64, so far
- * positions lose nothing); elements rot .. head_dim - 1 are copied.
+ * at the angle positions[t] * inv_freq[i] (formed and reduced in fp64 with what
+ * its products round off, so far positions lose nothing: off by less than
+ * 2^-49 of a turn at frequencies up to 1); elements rot .. head_dim - 1 are
+ * copied.
  *
  *   heads       host int32 [n_slices], heads of each slice, side by side from
  *               column x_col_off[i] of x (and y_col_off[i] of y).
