@@ -189,7 +189,7 @@ SHAPES = [(1, 1, 1), (1, 128, 128), (1, 4096, 4096), (2, 64, 14336), (3, 129, 25
           (17, 1501, 1000), (31, 384, 130), (32, 6144, 512), (33, 200, 2048), (48, 64, 16), (64, 2048, 2048),
           (65, 300, 384), (77, 1501, 1000), (128, 128, 8192), (129, 257, 513), (200, 513, 255), (256, 4096, 1024),
           (300, 72, 4104), (512, 1024, 896), (1000, 640, 1111), (1025, 1153, 200), (2048, 2304, 384),
-          # one for each tile and number of parts of K that the host chooses
+          # more of the tiles and parts of K that the host chooses (all: test_base_paths.py)
           (4, 1024, 4096), (5, 4000, 2050), (20, 4000, 2050), (24, 4000, 300), (130, 2000, 6200), (70, 4000, 300),
           (200, 4000, 300), (70, 10000, 200), (64, 19100, 200), (128, 19100, 200), (300, 6000, 300),
           (300, 4000, 5300), (700, 6000, 200)]
