@@ -13,6 +13,12 @@
 //
 // A wait that runs out (up to a second; never in a sound run) ends the kernel and
 // makes its outputs NaN.
+//
+// Tensor memory is allocated before the wait for the previous kernel, which may not
+// have allocated its own yet (the adapters' kernels let their successors start
+// first).  No CTA is starved by that, on this stream or another: a CTA that takes all
+// 512 columns fills its SM's shared memory, and of those that take up to 256 an SM
+// holds two.
 #include <string.h>
 
 #include <atomic>
@@ -49,10 +55,11 @@ __device__ __forceinline__ void drain_copies() {
 // block of 512 MMA clocks and pair.  Tensor memory then holds two blocks.
 //
 // What bounds it: the hand-over MMA -> promotion -> MMA, two blocks deep, whose
-// steps take 150 to 200 clocks each beside the copies; the tensor pipe is busy 56 %
-// of the time.  At 8192 x 28672 x 4096: 792 to 830 us (2.3 to 2.4 PFLOP/s) at full
-// clocks, 938 us in a long run, which stands at the power limit at 1.49 GHz.
-// Without the promotion's arithmetic: 750; without the MMAs: 508.
+// steps take 150 to 200 clocks each beside the copies; the tensor pipe is busy 65 %
+// of the time at 4096 x 8192 x 4096.  At 8192 x 28672 x 4096: 792 to 830 us (2.3 to
+// 2.4 PFLOP/s) at full clocks, 966 to 984 us in a long run, which stands at the power
+// limit at 1.49 GHz.  An earlier form took 750 without the promotion's arithmetic and
+// 508 without the MMAs.
 // ---------------------------------------------------------------------------
 constexpr int kWTile = 256;                 // tokens and outputs per pair
 constexpr int kWHalf = 128;                 // rows of A and of B that one CTA loads

@@ -11,9 +11,10 @@
 //
 // Bound: memory (2 bytes read and 2 written per element; 28.1 us at 8192 tokens
 // of 32 + 8 heads of 128, 6.0 TB/s), with norms nearly as much by the issue of
-// instructions (36.4 us; packed fp32 arithmetic needed more registers: 42.6).  A group of L lanes holds one head: each lane
-// the two vectors of V elements that its pairs join, so a half-split rotation
-// needs no exchange between lanes, and the norm needs one sum over the L lanes.
+// instructions (36.4 us; packed fp32 arithmetic needed more registers: 42.6).  A
+// group of L lanes holds one head: each lane the two vectors of V elements that its
+// pairs join, so a half-split rotation needs no exchange between lanes, and the
+// norm needs one sum over the L lanes.
 // The order of the table decides much: with (cos, sin) pairs in the order of the
 // pairs, lanes read it with 4-way bank conflicts, and the same call took 35 us.
 #include <math.h>
@@ -270,13 +271,17 @@ cudaError_t rope_tokens(const RopeArgs& a, bool norm, cudaStream_t st) {
                        : rope_launch<E, V, ITEMS, TPT, false>(a, norm, st);
 }
 
-// Two tokens per thread once that leaves several CTAs per SM.  With CTAs of 320
-// threads: 30.0 us against 33.8 at 8192 tokens of 40 heads of 128 (38.1 against
-// 47.2 with norms; four tokens 31.0 and 38.8), 3.6 against 3.3 at 512 tokens.
+// Two tokens per thread from 3840 lanes for each of the 148 SMs on, enough to fill
+// them with half the threads: at 40 heads of 128, 14.1 us against 16.1 at 3750
+// tokens (17.9 against 20.2 with norms), 8.1 against 8.7 at 1776, but 4.9 against
+// 4.7 at 937 and 4.6 against 3.8 at 625.  Four tokens were slower than two (31.0 us
+// against 30.0 at 8192 tokens in the form of then).
+constexpr int64_t kTwoTokenLanes = 148 * 3840;
+
 template <typename E, int V, int ITEMS>
 cudaError_t rope_layout(const RopeArgs& a, bool norm, cudaStream_t st) {
   const int64_t lanes = (int64_t)a.T * a.head_end[a.n_slices - 1] * (a.dim / 2 / V / ITEMS);
-  return lanes >= 2 * 6 * 148 * 320 ? rope_tokens<E, V, ITEMS, 2>(a, norm, st)
+  return lanes >= kTwoTokenLanes ? rope_tokens<E, V, ITEMS, 2>(a, norm, st)
                                     : rope_tokens<E, V, ITEMS, 1>(a, norm, st);
 }
 

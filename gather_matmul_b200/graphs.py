@@ -39,7 +39,8 @@ class LoraGraphSet:
         self.stream = stream if stream is not None else torch.cuda.Stream()
         self.graphs: Dict[bool, torch.cuda.CUDAGraph] = {}
         # library kernels recorded into each graph (lora_launch_count across
-        # the capture): 0 for the graph without LoRA
+        # the capture): for the graph without LoRA the base products' and
+        # rotations' alone, 0 if the step makes none
         self.lora_launches: Dict[bool, int] = {}
 
     def capture(self, keep_graph: bool = False) -> "LoraGraphSet":

@@ -394,6 +394,7 @@ LORA_API lora_status lora_shrink_noalloc(lora_dtype dtype, int T, int D, int r, 
  *   x      device [T, ldx] dtype, ldx >= K a multiple of 8.
  *   q      device [T, ldq] bytes, ldq >= K a multiple of 16.
  *   scale  device fp32 [ceil(T / block_rows), ceil(K / 128)] contiguous.
+ * q and scale must not overlap x.
  * 0 <= T <= LORA_MAX_TOKENS, 1 <= K <= LORA_MAX_WIDTH.  One launch.
  */
 LORA_API lora_status lora_quantize_fp8(lora_dtype dtype, int T, int K, int block_rows,
@@ -481,9 +482,9 @@ LORA_API lora_status lora_rope_frequencies(int rot, double base, lora_rope_kind 
  *   attn_scale * (a cos - b sin),  attn_scale * (b cos + a sin)
  *
  * at the angle positions[t] * inv_freq[i] (formed and reduced in fp64 with what
- * its products round off, so far positions lose nothing: off by less than
- * 2^-49 of a turn at frequencies up to 1); elements rot .. head_dim - 1 are
- * copied.
+ * its products round off, so far positions lose nothing: within 2^-52 of a
+ * turn at frequencies up to 1, then rounded to fp32 once); elements
+ * rot .. head_dim - 1 are copied.
  *
  *   heads       host int32 [n_slices], heads of each slice, side by side from
  *               column x_col_off[i] of x (and y_col_off[i] of y).
