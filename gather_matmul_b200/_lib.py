@@ -27,6 +27,9 @@ LORA_FP8_BLOCK = 128
 LORA_MAX_WIDTH = 1 << 20
 LORA_MAX_HEAD_DIM = 256
 LORA_MAX_HEADS = 4096
+LORA_MAX_PAGES = 1 << 22
+LORA_MAX_SEQS = 1 << 16
+LORA_MAX_FORKS = 4096
 ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 # Every symbol the header declares, with (restype, argtypes).
@@ -66,6 +69,16 @@ SIGNATURES = {
                          _vp, _f32, _i32, _vp]),
     "lora_norm_rope": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _f32, _vp,
                               _i64, _vp, _vp, _vp, _f32, _i32, _vp]),
+    "lora_cache_workspace_bytes": (_sz, [_i32, _i32]),
+    "lora_cache_write": (_i32, [_i32] * 8 + [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                             _vp]),
+    "lora_cache_attention": (_i32, [_i32] * 9 + [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _vp,
+                                                 _i64, _vp, _sz, _vp]),
+    "lora_pages_extend": (_i32, [_i32] * 4 + [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "lora_pages_free": (_i32, [_i32] * 3 + [_vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "lora_pages_fork": (_i32, [_i32] * 7 + [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "lora_pages_compact": (_i32, [_i32] * 7 + [_vp] * 8 + [_sz, _vp]),
+    "lora_pages_copy": (_i32, [_i32] * 5 + [_vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
     "lora_status_string": (ctypes.c_char_p, [_i32]),
     "lora_build_info": (ctypes.c_char_p, []),
     "lora_launch_count": (ctypes.c_ulonglong, []),

@@ -1,0 +1,479 @@
+// Attention of few queries over the paged 8-bit cache (lora_cache_attention):
+// single tokens, where every k and v byte is used by one sequence's rows only and
+// the kernel is bound by reading them.
+//
+//   s_rj = c q_r . k_j,   o_r = sum_j 2^(s_rj - m) v_j / sum_j 2^(s_rj - m)
+//
+// with c = softmax scale * log2 e.  A page's v scale enters as its logarithm: with
+// t = s + log2 v_scale the numerators' weights 2^(t - m) are at most 2^kShift, so
+// that they round to fp16 as they are (11 bits), whatever the scales, and the
+// denominators' terms are 2^(t - m) / v_scale in fp32.  m is a running maximum of t
+// that is only raised when a term would pass 2^(kShift + kSlack).
+//
+// Products run on mma.sync with the tokens (k) and the head's elements (v) on the
+// wide side, M = 16, and the rows on the narrow one, N = 8: a tile of 8 rows costs
+// half of what it would cost as M = 16.  e4m3 becomes fp16 exactly, in registers.
+// The order of the products' inner indices is free, so every thread copies 16-byte
+// pieces of its own (cp.async) and reads back just those: no transposes, no
+// barriers, and what is in flight sits in shared memory.  q's rows are brought to
+// fp16 by powers of two (their largest elements to 2^7 .. 2^8), which costs less
+// than the rounding of the sums.
+#include <cfloat>
+
+#include "cache_attn.cuh"
+#include "internal.h"
+
+namespace lora {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kFThreads = 128, kFWarps = 4;
+constexpr int kFUnit = 64;                  // tokens of a unit: 16 for each warp
+constexpr float kShift = 6.f, kSlack = 8.f;
+
+template <int D> struct FewShape;           // stages, and CTAs that share an SM
+template <> struct FewShape<64> { static constexpr int kStages = 6; };
+template <> struct FewShape<128> { static constexpr int kStages = 3; };
+template <> struct FewShape<192> { static constexpr int kStages = 3; };
+template <> struct FewShape<256> { static constexpr int kStages = 3; };
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// two e4m3 codes (low byte first) to two halves
+__device__ __forceinline__ uint32_t halves(uint32_t two) {
+  uint32_t h;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(two));
+  return h;
+}
+__device__ __forceinline__ uint32_t halves_hi(uint32_t two) {
+  uint32_t h;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(h) : "r"(two));
+  return h;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Partial sums of a row tile: [R][D] weighted values, then [R][2] maximum and sum.
+template <int D, int NT>
+__device__ __forceinline__ float* part_of(const AttnArgs& a, int cta, int which) {
+  return a.part + (size_t)(2 * cta + which) * (8 * NT) * (D + 2);
+}
+
+// dims d, d + 1 of a row of y
+template <typename E>
+__device__ __forceinline__ void put_row(const AttnArgs& a, const Tile& t, int h, int row, int d, float x, float y) {
+  const int r = t.r0 + row, i = r / a.group;
+  E* out = static_cast<E*>(a.y) + (int64_t)(t.q0 + i) * a.ldy + ((int64_t)h * a.group + (r - i * a.group)) * a.dim + d;
+  *reinterpret_cast<uint32_t*>(out) = Elem<E>::pack2(x, y);
+}
+
+template <int D, int NT, typename E>
+__global__ void __launch_bounds__(kFThreads, D <= 128 ? (NT == 1 ? 4 : 3) : 2)
+attention_few_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int R = 8 * NT, ST = FewShape<D>::kStages;
+  constexpr int KP = D / 32;               // 16-byte pieces of k that a thread holds: 2 tokens, D / 4 each
+  constexpr int KT = D / 64;               //   of one token
+  constexpr int MT = D / 16;               // m-tiles of the v product, and words of k of a token
+  constexpr int VB = D / 8;                // bytes of v of one token (4 tokens)
+  constexpr int NP = D / 16;               // 16-byte pieces in all
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Shared sh;
+  __shared__ float2 scales[ST][kFWarps];
+  __shared__ float stat[kFWarps][R][2];
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+
+  unsigned long long w0, w1, all;
+  int ctas;
+  divide<R, kFUnit>(a, sh, 2, w0, w1, all, ctas);
+  if (w0 >= w1) return;
+  int64_t slot = sh.slot;
+  int seq = sh.seq;
+  unsigned long long off = sh.off, w = w0;
+  const int page = 1 << a.page_log;
+  const int64_t head_bytes = (int64_t)a.dim << a.page_log;
+
+  while (w < w1) {
+    Tile t;
+    while (seq + 1 < a.B && slot_of<R>(a, seq + 1) <= slot) ++seq;
+    tile_of<R, kFUnit>(a, seq, slot, t);
+    const unsigned long long slot_units = (unsigned long long)t.units * a.Hk;
+    if (off >= slot_units) {                // this slot is done (or holds no rows)
+      off -= slot_units;
+      ++slot;
+      continue;
+    }
+    const int h = (int)(off / t.units), ua = (int)(off - (unsigned long long)h * t.units);
+    const int nu = (int)min((unsigned long long)(t.units - ua), w1 - w);
+    const unsigned long long item0 = w - ua, item1 = item0 + t.units;
+
+    // ---- copies: iteration it of this warp takes tokens tok0 + it * kFUnit .. + 16
+    const int tok0 = (t.u0 + ua) * kFUnit + warp * 16;
+    const uint8_t* base = a.cache + (int64_t)h * head_bytes;
+    const int64_t v_off = (int64_t)a.Hk * head_bytes, page_bytes = 2 * v_off;
+    int pids = -1;
+    auto fetch_pids = [&](int it) {
+      const int tok = tok0 + (it + lane) * kFUnit;
+      pids = -1;
+      if (it + lane < nu && tok < t.hi && tok + 16 > t.lo) {
+        pids = a.tables[(int64_t)t.b * a.M + (tok >> a.page_log)];
+        if (pids < 0 || pids >= a.P) {
+          atomicAdd(a.bad, 1);
+          pids = -1;
+        }
+      }
+    };
+    unsigned ready = 0;                     // bit s: stage s holds tokens
+    auto issue = [&](int it) {
+      if ((it & 31) == 0) fetch_pids(it);
+      const int s = it % ST;
+      const int pid = __shfl_sync(~0u, pids, it & 31);
+      ready &= ~(1u << s);
+      if (it < nu && pid >= 0) {
+        ready |= 1u << s;
+        const int tok = tok0 + it * kFUnit, in_page = tok & (page - 1);
+        const uint8_t* k = base + (int64_t)pid * page_bytes + (int64_t)in_page * a.dim;
+        const uint8_t* v = k + v_off;
+        const uint32_t dst = ptx::smem_u32(smem) + (uint32_t)(s * NP * kFThreads + tid) * 16;
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {      // tokens g and g + 8, elements from c D / 4 on
+          const int e = c * (D / 4) + 16 * (i % KT);
+          copy16(dst + (uint32_t)i * kFThreads * 16, k + (int64_t)(g + 8 * (i / KT)) * a.dim + (e < a.dim ? e : 0), e < a.dim);
+        }
+        const uint32_t vd = ptx::smem_u32(smem) + (uint32_t)(s * NP + KP) * kFThreads * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {       // tokens 2c, 2c + 1, 2c + 8, 2c + 9, elements from g D / 8 on
+          const int tk = 2 * c + (i & 1) + 8 * (i >> 1);
+          const bool in = tok + tk < t.hi;  // what lies behind may be anything: zeros in its place
+          if constexpr (VB % 16 == 0) {
+#pragma unroll
+            for (int j = 0; j < VB / 16; ++j) {
+              const int e = g * VB + 16 * j;
+              const bool ok = in && e < a.dim;
+              copy16(vd + (uint32_t)((i * (VB / 16) + j) * kFThreads + tid) * 16, v + (ok ? (int64_t)tk * a.dim + e : 0), ok);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < VB / 8; ++j) {
+              const int e = g * VB + 8 * j;
+              const bool ok = in && e < a.dim;
+              copy8(vd + (uint32_t)((i * (VB / 8) + j) * kFThreads + tid) * 8, v + (ok ? (int64_t)tk * a.dim + e : 0), ok);
+            }
+          }
+        }
+        if (lane < 2)
+          copy4(ptx::smem_u32(&scales[s][warp]) + 4 * lane, a.scale + ((int64_t)pid * 2 + lane) * a.Hk + h);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int it = 0; it < ST - 1; ++it) issue(it);
+
+    // ---- q: row 8 nt + g of the tile, elements c D / 4 .. of it
+    uint32_t q[NT][MT][2];
+    float cs[NT][2];                        // c * the power of two, of rows 2c and 2c + 1
+    int pos[NT][2];                         // their positions; -1: no such row
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = 8 * nt + g, r = t.r0 + row, i = r / a.group;
+      const bool in = row < t.rows;
+      const E* src = static_cast<const E*>(a.q) + (int64_t)(t.q0 + (in ? i : 0)) * a.ldq +
+                     ((int64_t)h * a.group + (in ? r - i * a.group : 0)) * a.dim + c * (D / 4);
+      uint4 v[2 * KT];
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2 * KT; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (in && c * (D / 4) + 8 * j < a.dim) v[j] = ldg_nc(src + 8 * j);
+        float f[8];
+        Elem<E>::to_f32(v[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      // 2^k brings the largest element to 2^7 .. 2^8
+      const int k = min(max(7 + 127 - (int)(__float_as_uint(top) >> 23), -120), 120);
+      const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+      for (int j = 0; j < 2 * KT; ++j) {
+        float f[8];
+        Elem<E>::to_f32(v[j], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          q[nt][2 * j + e / 2][e & 1] = Elem<__half>::pack2(f[2 * e] * up, f[2 * e + 1] * up);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row2 = 8 * nt + 2 * c + e;
+        cs[nt][e] = a.c * __shfl_sync(~0u, down, (2 * c + e) * 4);
+        pos[nt][e] = row2 < t.rows ? t.len - t.n + (t.r0 + row2) / a.group : -1;
+      }
+    }
+    const int pos_low = t.len - t.n + t.r0 / a.group, pos_high = t.len - t.n + (t.r0 + t.rows - 1) / a.group;
+
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = -FLT_MAX;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    for (int it = 0; it < nu; ++it) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+      __syncwarp();                         // the scales came by lanes 0 and 1
+      const int s = it % ST;
+      const bool have = (ready >> s) & 1;
+      issue(it + ST - 1);
+      if (!have) continue;
+      const int tok = tok0 + it * kFUnit;
+      const uint4* mine = reinterpret_cast<const uint4*>(smem) + (size_t)s * NP * kFThreads + tid;
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KT; ++j) {
+        const uint4 lo = mine[j * kFThreads], hi = mine[(KT + j) * kFThreads];
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t af[4] = {halves(wl[i]), halves(wh[i]), halves_hi(wl[i]), halves_hi(wh[i])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            ptx::mma_16816<false>(sc[nt], af, q[nt][4 * j + i][0], q[nt][4 * j + i][1]);
+        }
+      }
+      const float2 kv = scales[s][warp];
+      const float lv = log2f(kv.y), inv = 1.f / kv.y;
+      const bool edge = tok + 15 > pos_low || (a.window > 0 && tok <= pos_high - a.window);
+      uint32_t p[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmaf(sc[nt][i], kv.x * cs[nt][i & 1], lv);
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = tok + g + 8 * (i >> 1), at = pos[nt][i & 1];
+            if (j > at || (a.window > 0 && j <= at - a.window)) x[i] = -INFINITY;
+          }
+        }
+        const float t0 = fmaxf(x[0], x[2]), t1 = fmaxf(x[1], x[3]);
+        if (__any_sync(~0u, t0 > m[nt][0] + kSlack || t1 > m[nt][1] + kSlack)) {
+          float n0 = fmaxf(m[nt][0], t0), n1 = fmaxf(m[nt][1], t1);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) {
+            n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, d));
+            n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, d));
+          }
+          const float f0 = exp2_fast(m[nt][0] - n0), f1 = exp2_fast(m[nt][1] - n1);
+          m[nt][0] = n0;
+          m[nt][1] = n1;
+          l[nt][0] *= f0;
+          l[nt][1] *= f1;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[nt][i][0] *= f0;
+            o[nt][i][1] *= f1;
+            o[nt][i][2] *= f0;
+            o[nt][i][3] *= f1;
+          }
+        }
+        const float b0 = m[nt][0] - kShift, b1 = m[nt][1] - kShift;
+        const float e0 = exp2_fast(x[0] - b0), e1 = exp2_fast(x[1] - b1);
+        const float e2 = exp2_fast(x[2] - b0), e3 = exp2_fast(x[3] - b1);
+        l[nt][0] = fmaf(e0 + e2, inv, l[nt][0]);
+        l[nt][1] = fmaf(e1 + e3, inv, l[nt][1]);
+        p[nt][0] = transpose8x8(Elem<__half>::pack2(e0, e1));
+        p[nt][1] = transpose8x8(Elem<__half>::pack2(e2, e3));
+      }
+      // v: words of 4 elements of the 4 tokens -> pairs of tokens of one element
+      uint32_t wv[4][VB / 4];
+      if constexpr (VB % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < VB / 16; ++j) {
+            const uint4 v = mine[(KP + i * (VB / 16) + j) * kFThreads];
+            wv[i][4 * j] = v.x, wv[i][4 * j + 1] = v.y, wv[i][4 * j + 2] = v.z, wv[i][4 * j + 3] = v.w;
+          }
+      } else {
+        const uint2* m2 = reinterpret_cast<const uint2*>(reinterpret_cast<const uint4*>(smem) + (size_t)(s * NP + KP) * kFThreads) + tid;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < VB / 8; ++j) {
+            const uint2 v = m2[(i * (VB / 8) + j) * kFThreads];
+            wv[i][2 * j] = v.x, wv[i][2 * j + 1] = v.y;
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < VB / 4; ++j) {
+        const uint32_t x0 = __byte_perm(wv[0][j], wv[1][j], 0x5140), x1 = __byte_perm(wv[0][j], wv[1][j], 0x7362);
+        const uint32_t y0 = __byte_perm(wv[2][j], wv[3][j], 0x5140), y1 = __byte_perm(wv[2][j], wv[3][j], 0x7362);
+        const uint32_t a0[4] = {halves(x0), halves_hi(x0), halves(y0), halves_hi(y0)};
+        const uint32_t a1[4] = {halves(x1), halves_hi(x1), halves(y1), halves_hi(y1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          ptx::mma_16816<false>(o[nt][2 * j], a0, p[nt][0], p[nt][1]);
+          ptx::mma_16816<false>(o[nt][2 * j + 1], a1, p[nt][0], p[nt][1]);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // ---- the warps' sums meet in shared memory, in the stages' place.  Element
+    // g VB + 2 mt + e of a row lies at mt 16 + 2 g + e: neighbouring lanes write
+    // neighbouring words.
+    constexpr int LD = D + 8;
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(~0u, sum, d);
+        const int row = 8 * nt + 2 * c + e;
+        if (g == 0) {
+          stat[warp][row][0] = m[nt][e];
+          stat[warp][row][1] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          *reinterpret_cast<float2*>(acc + ((size_t)warp * R + row) * LD + 16 * i + 2 * g) =
+              make_float2(o[nt][i][e], o[nt][i][2 + e]);
+      }
+    }
+    __syncthreads();
+    const bool whole = w == item0 && w + nu == item1;
+    const int which = w == item0 ? 1 : 0;   // an item begun here and not ended is this CTA's last
+    float* part = part_of<D, NT>(a, blockIdx.x, which);
+    for (int i = tid; i < t.rows * (D / 2); i += kFThreads) {
+      const int row = i / (D / 2), pr = i % (D / 2), gg = pr / MT, mt = pr % MT, d = gg * VB + 2 * mt;
+      float top = stat[0][row][0];
+#pragma unroll
+      for (int k = 1; k < kFWarps; ++k) top = fmaxf(top, stat[k][row][0]);
+      float x = 0.f, y = 0.f, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kFWarps; ++k) {
+        const float f = exp2_fast(stat[k][row][0] - top);
+        const float2 v = *reinterpret_cast<const float2*>(acc + ((size_t)k * R + row) * LD + 16 * mt + 2 * gg);
+        x = fmaf(v.x, f, x);
+        y = fmaf(v.y, f, y);
+        sum = fmaf(stat[k][row][1], f, sum);
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (d < a.dim) put_row<E>(a, t, h, row, d, x * inv, y * inv);
+      } else {
+        __stcg(reinterpret_cast<float2*>(part + (size_t)row * D + d), make_float2(x, y));
+        if (pr == 0) __stcg(reinterpret_cast<float2*>(part + (size_t)R * D + 2 * row), make_float2(top, sum));
+      }
+    }
+    if (!whole) {
+      const int first = owner(item0, all, ctas), last = owner(item1 - 1, all, ctas);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int come = atomicAdd(a.join + first, 1);
+        sh.flag = come == last - first;
+        if (sh.flag) a.join[first] = 0;     // as the next call finds it
+      }
+      __syncthreads();
+      if (sh.flag) {
+        __threadfence();
+        for (int i = tid; i < t.rows * (D / 2); i += kFThreads) {
+          const int row = i / (D / 2), d = 2 * (i % (D / 2));
+          if (d >= a.dim) continue;
+          float top = -FLT_MAX, x = 0.f, y = 0.f, sum = 0.f;
+          for (int k = first; k <= last; ++k) {
+            const float* pk = part_of<D, NT>(a, k, k == first ? 1 : 0);
+            const float2 ms = __ldcg(reinterpret_cast<const float2*>(pk + (size_t)R * D + 2 * row));
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(pk + (size_t)row * D + d));
+            const float up = fmaxf(top, ms.x), f0 = exp2_fast(top - up), f1 = exp2_fast(ms.x - up);
+            x = x * f0 + v.x * f1;
+            y = y * f0 + v.y * f1;
+            sum = sum * f0 + ms.y * f1;
+            top = up;
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          put_row<E>(a, t, h, row, d, x * inv, y * inv);
+        }
+      }
+    }
+    __syncthreads();                        // the stages are free again
+    w += nu;
+    off += nu;
+  }
+}
+
+template <int D, int NT, typename E>
+cudaError_t few_launch(const AttnArgs& a, cudaStream_t st) {
+  constexpr int stage = FewShape<D>::kStages * (D / 16) * kFThreads * 16;
+  constexpr int acc = kFWarps * 8 * NT * (D + 8) * 4;
+  constexpr int smem = stage > acc ? stage : acc;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(attention_few_kernel<D, NT, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  constexpr int per_sm = D <= 128 ? (NT == 1 ? 4 : 3) : 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(148 * per_sm, 1, 1);
+  cfg.blockDim = dim3(kFThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return counted_launch(cudaLaunchKernelEx(&cfg, attention_few_kernel<D, NT, E>, a));
+}
+
+template <int D, typename E>
+cudaError_t few_rows(const AttnArgs& a, cudaStream_t st) {
+  return a.starts == nullptr && a.group <= 8 ? few_launch<D, 1, E>(a, st) : few_launch<D, 2, E>(a, st);
+}
+
+template <typename E>
+cudaError_t few_width(const AttnArgs& a, cudaStream_t st) {
+  if (a.dim <= 64) return few_rows<64, E>(a, st);
+  if (a.dim <= 128) return few_rows<128, E>(a, st);
+  if (a.dim <= 192) return few_rows<192, E>(a, st);
+  return few_rows<256, E>(a, st);
+}
+
+}  // namespace
+
+// parts of the widest tile: 2 of a CTA
+size_t CacheWork::part_floats(int dim) {
+  const int D = (dim + 63) / 64 * 64;
+  return (size_t)2 * 148 * 4 * kFewRows * (D + 2);
+}
+
+cudaError_t launch_attention_few(lora_dtype dt, const AttnArgs& a, cudaStream_t st) {
+  return dt == LORA_BF16 ? few_width<__nv_bfloat16>(a, st) : few_width<__half>(a, st);
+}
+
+}  // namespace lora

@@ -14,6 +14,8 @@ and streams.
   check_errors(meta)                           device-side bad-index report
   quantize_fp8 / matmul_fp8 / linear_fp8       the base product y = x W^T in block-scaled e4m3
   rope / norm_rope / rope_frequencies          rotation (and norms) of q and k head slices
+  cache_write / cache_attention                a paged 8-bit k/v cache: its write, attention over it
+  pages_extend / _fork / _free / _compact / _copy   its pages
 
 has_active: the per-token calls take the host flag of the C ABI.  Left as
 None, it is derived from `idx_host` (a host copy of the batch's indices, as a
@@ -495,6 +497,210 @@ def norm_rope(x: torch.Tensor, weights, y: torch.Tensor, heads: Sequence[int], h
     _check("lora_norm_rope", _lib.load().lora_norm_rope(
         *head, ws, eps, *tail, attn_scale, bool(interleaved), st))
     return y
+
+
+# ---------------------------------------------------------------------------
+# Behind the attention inputs: a paged key/value cache in 8 bits.  cache:
+# float8_e4m3fn [P, 2, kv_heads, page_tokens, head_dim] of one layer, scale:
+# float32 [P, 2, kv_heads]; the moves of pages take those of all layers, with a
+# leading dimension.  tables: int32 [B, pages of a sequence], -1 = none;
+# lengths: int32 [B]; refs: int32 [P].  Tensors must lie on the current CUDA
+# device.
+# ---------------------------------------------------------------------------
+def _ints(t, name, shape):
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.shape != shape:
+        raise TypeError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _list(t, name):
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.dim() != 1:
+        raise TypeError(f"{name} must be a contiguous int32 tensor of one dimension")
+    return _int(name, t.numel())
+
+
+def _cache(cache, scale, layers):
+    """(layers, pages, kv_heads, page_tokens, head_dim); layers 0: of one layer, without that dimension."""
+    if cache.dtype is not _FP8 or not cache.is_contiguous() or cache.dim() != 5 + layers or \
+            cache.shape[1 + layers] != 2:
+        raise TypeError("cache must be a contiguous float8_e4m3fn tensor of " +
+                        ("layers x " if layers else "") + "pages x 2 x kv_heads x page_tokens x head_dim")
+    if scale.dtype is not torch.float32 or not scale.is_contiguous() or \
+            scale.shape != cache.shape[:3 + layers]:
+        raise TypeError("scale must be a contiguous float32 tensor of the cache's first dimensions")
+    shape = tuple(_int("cache", v) for v in cache.shape)
+    return (shape[0] if layers else 1, shape[layers], *shape[2 + layers:])
+
+
+def _seqs(tables, lengths=None):
+    if tables.dtype is not torch.int32 or not tables.is_contiguous() or tables.dim() != 2:
+        raise TypeError("tables must be a contiguous int32 tensor of sequences x pages")
+    B, M = tables.shape
+    if lengths is not None:
+        _ints(lengths, "lengths", (B,))
+    return _int("tables", B), _int("tables", M)
+
+
+def _work(work):
+    if not work.is_contiguous():
+        raise ValueError("work must be contiguous")
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
+def cache_workspace(n_pages: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for the calls on a cache of n_pages pages; one
+    for each stream that such calls run on."""
+    call = "lora_cache_workspace_bytes"
+    n = _lib.load().lora_cache_workspace_bytes(_int(call, n_pages), _int(call, head_dim))
+    if n == 0:
+        raise LoraError(call, _lib.LORA_ERR_UNSUPPORTED)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _new_rows(t, name, width, starts, B, T=None, dtype=None):
+    ld = _rows(t, name, dtype)
+    if t.shape[1] != width or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} must be [T, heads * head_dim] = [{t.shape[0] if T is None else T}, {width}]")
+    if starts is None and t.shape[0] != B:
+        raise ValueError("without starts there is one row for each sequence")
+    return ld
+
+
+def cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor,
+                tables: torch.Tensor, lengths: torch.Tensor, work: torch.Tensor,
+                starts: Optional[torch.Tensor] = None, stream=None):
+    """Put the new tokens' keys and values (fp16/bf16 [T, kv_heads * head_dim],
+    columns of one matrix or not) into their sequences' pages in e4m3, with one
+    power of two as scale for each (page, k or v, head).
+
+    lengths: tokens of each sequence, the new ones counted in; starts: int32
+    [B + 1], the new tokens of sequence b are rows starts[b] .. starts[b+1]
+    (None: one row each); the pages must be there (pages_extend)."""
+    _, P, H, page, dim = _cache(cache, scale, 0)
+    B, M = _seqs(tables, lengths)
+    T = k.shape[0]
+    ldk = _new_rows(k, "k", H * dim, starts, B)
+    ldv = _new_rows(v, "v", H * dim, starts, B, T, k.dtype)
+    given = () if starts is None else (starts,)
+    if starts is not None:
+        _ints(starts, "starts", (B + 1,))
+    wp, wn = _work(work)
+    st = _here(stream, k, v, cache, scale, tables, lengths, work, *given)
+    _check("lora_cache_write", _lib.load().lora_cache_write(
+        _dtype(k), T, B, H, dim, page, P, M, k.data_ptr(), ldk, v.data_ptr(), ldv, cache.data_ptr(),
+        scale.data_ptr(), tables.data_ptr(), lengths.data_ptr(),
+        None if starts is None else starts.data_ptr(), wp, wn, st))
+
+
+def cache_attention(q: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor, tables: torch.Tensor,
+                    lengths: torch.Tensor, y: torch.Tensor, work: torch.Tensor,
+                    starts: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+                    window: int = 0, stream=None) -> torch.Tensor:
+    """y = softmax(softmax_scale q k^T) v of the new tokens' queries over the
+    tokens of their sequences up to themselves (the last `window` of them only,
+    if window > 0).  q, y: fp16/bf16 [T, q_heads * head_dim]; lengths, starts as
+    for cache_write, which comes first; softmax_scale: 1 / sqrt(head_dim) by
+    default.  Queries that see nothing get zeros."""
+    _, P, H, page, dim = _cache(cache, scale, 0)
+    B, M = _seqs(tables, lengths)
+    T, width = q.shape[0], q.shape[1] if q.dim() == 2 else -1
+    if width <= 0 or width % (H * dim):
+        raise ValueError("q must hold a multiple of the cache's heads")
+    ldq = _new_rows(q, "q", width, starts, B)
+    ldy = _new_rows(y, "y", width, starts, B, T, q.dtype)
+    given = () if starts is None else (starts,)
+    if starts is not None:
+        _ints(starts, "starts", (B + 1,))
+    wp, wn = _work(work)
+    st = _here(stream, q, cache, scale, tables, lengths, y, work, *given)
+    _check("lora_cache_attention", _lib.load().lora_cache_attention(
+        _dtype(q), T, B, width // dim, H, dim, page, P, M, q.data_ptr(), ldq, cache.data_ptr(),
+        scale.data_ptr(), tables.data_ptr(), lengths.data_ptr(),
+        None if starts is None else starts.data_ptr(),
+        dim ** -0.5 if softmax_scale is None else softmax_scale, _int("window", window),
+        y.data_ptr(), ldy, wp, wn, st))
+    return y
+
+
+def pages_extend(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_tokens: int,
+                 work: torch.Tensor, stream=None):
+    """Free pages, lowest first, for the places of each sequence's table that
+    its length needs and that hold none yet."""
+    B, M = _seqs(tables, lengths)
+    P = _list(refs, "refs")
+    wp, wn = _work(work)
+    st = _here(stream, tables, lengths, refs, work)
+    _check("lora_pages_extend", _lib.load().lora_pages_extend(
+        B, M, _int("page_tokens", page_tokens), P, tables.data_ptr(), lengths.data_ptr(),
+        refs.data_ptr(), wp, wn, st))
+
+
+def pages_free(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, seqs: torch.Tensor,
+               work: torch.Tensor, stream=None):
+    """The listed sequences (int32 [n]) end: their pages' counts go down by one,
+    their rows become -1 and their lengths 0."""
+    B, M = _seqs(tables, lengths)
+    P, n = _list(refs, "refs"), _list(seqs, "seqs")
+    wp, wn = _work(work)
+    st = _here(stream, tables, lengths, refs, seqs, work)
+    _check("lora_pages_free", _lib.load().lora_pages_free(
+        B, M, P, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(), seqs.data_ptr(), n, wp, wn,
+        st))
+
+
+def pages_fork(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, src: torch.Tensor,
+               dst: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor, work: torch.Tensor,
+               stream=None):
+    """Each empty row dst[i] becomes a copy of the sequence src[i] (int32 [n]):
+    full pages are shared, the begun last one is copied in all layers."""
+    B, M = _seqs(tables, lengths)
+    L, P, H, page, dim = _cache(cache, scale, 1)
+    _ints(refs, "refs", (P,))
+    n = _list(src, "src")
+    _ints(dst, "dst", (n,))
+    wp, wn = _work(work)
+    st = _here(stream, tables, lengths, refs, src, dst, cache, scale, work)
+    _check("lora_pages_fork", _lib.load().lora_pages_fork(
+        B, M, L, H, dim, page, P, tables.data_ptr(), lengths.data_ptr(), refs.data_ptr(),
+        src.data_ptr(), dst.data_ptr(), n, cache.data_ptr(), scale.data_ptr(), wp, wn, st))
+
+
+def pages_compact(tables: torch.Tensor, refs: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor,
+                  work: torch.Tensor, out_tables: Optional[torch.Tensor] = None,
+                  out_refs: Optional[torch.Tensor] = None, n_live: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Move the live pages to the front of the pool in all layers; the tables
+    and counts follow, in place or into out_tables and out_refs.  n_live: int32
+    [1], receives the number of live pages."""
+    B, M = _seqs(tables)
+    L, P, H, page, dim = _cache(cache, scale, 1)
+    _ints(refs, "refs", (P,))
+    out_tables = tables if out_tables is None else out_tables
+    out_refs = refs if out_refs is None else out_refs
+    _ints(out_tables, "out_tables", (B, M))
+    _ints(out_refs, "out_refs", (P,))
+    given = () if n_live is None else (n_live,)
+    if n_live is not None:
+        _ints(n_live, "n_live", (1,))
+    wp, wn = _work(work)
+    st = _here(stream, tables, refs, cache, scale, work, out_tables, out_refs, *given)
+    _check("lora_pages_compact", _lib.load().lora_pages_compact(
+        B, M, L, H, dim, page, P, tables.data_ptr(), refs.data_ptr(), out_tables.data_ptr(),
+        out_refs.data_ptr(), None if n_live is None else n_live.data_ptr(), cache.data_ptr(),
+        scale.data_ptr(), wp, wn, st))
+
+
+def pages_copy(cache: torch.Tensor, scale: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+               work: torch.Tensor, stream=None):
+    """Copy page src[i] to page dst[i] (int32 [n]) in all layers, with its
+    scales.  No page may be the target of two pairs, or target and source."""
+    L, P, H, page, dim = _cache(cache, scale, 1)
+    n = _list(src, "src")
+    _ints(dst, "dst", (n,))
+    wp, wn = _work(work)
+    st = _here(stream, cache, scale, src, dst, work)
+    _check("lora_pages_copy", _lib.load().lora_pages_copy(
+        L, H, dim, page, P, cache.data_ptr(), scale.data_ptr(), src.data_ptr(), dst.data_ptr(), n,
+        wp, wn, st))
 
 
 def check_errors(meta: torch.Tensor, stream=None) -> int:

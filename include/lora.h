@@ -524,6 +524,168 @@ LORA_API lora_status lora_norm_rope(lora_dtype dtype, int T, int head_dim, int r
                                     const int64_t* positions, const double* inv_freq,
                                     float attn_scale, int interleaved, lora_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Behind the attention inputs: a paged key/value cache in 8 bits, its write,
+ * the attention that reads it, and the moves of its pages.
+ *
+ *   cache    device e4m3 [n_pages, 2, kv_heads, page_tokens, head_dim] for each
+ *            layer: a page holds page_tokens tokens of one sequence, the k of
+ *            every head, then the v.
+ *   scale    device fp32 [n_pages, 2, kv_heads] for each layer: the factor of
+ *            the values of (page, k or v, head), within 2^-32 .. 2^32, or NaN.
+ *            lora_cache_write makes powers of two; other factors are read as
+ *            they are.
+ *   tables   device int32 [n_seqs, max_pages]: the pages of each sequence in
+ *            order, its held ones first, -1 behind them.  One table serves all
+ *            layers.
+ *   lengths  device int32 [n_seqs]: tokens of each sequence, 0 for a row that
+ *            holds none.  A call that takes new tokens counts them in.
+ *   refs     device int32 [n_pages]: how many sequences hold each page; pages of
+ *            0 are free.
+ *   starts   device int32 [n_seqs + 1], 0 = starts[0] <= ... : the new tokens of
+ *            sequence b are rows starts[b] .. starts[b+1] of the call's tensors,
+ *            the last ones of its length; rows from starts[n_seqs] on are neither
+ *            read nor written.  NULL: row b is the one new token of sequence b
+ *            (then T = n_seqs).
+ *   work     device workspace of lora_cache_workspace_bytes(n_pages, head_dim),
+ *            256-byte aligned, zero-filled once before its first use; it serves
+ *            every call on a cache of that many pages.  Calls that may run at
+ *            the same time (two streams, two graphs) need one each.
+ *
+ * page_tokens is 16, 32, 64 or 128, head_dim a multiple of 16 up to
+ * LORA_MAX_HEAD_DIM, n_pages at most LORA_MAX_PAGES, n_seqs at most
+ * LORA_MAX_SEQS, max_pages * 128 below 2^31.
+ * A table entry that is no page where one is needed, and whatever else only the
+ * device can see to be wrong, is left out and counted in the workspace:
+ * lora_check_errors(work, ...) then returns LORA_ERR_BAD_INDEX.  The lists that a
+ * call takes must not share memory with what it writes.
+ * ------------------------------------------------------------------------ */
+#define LORA_MAX_PAGES (1 << 22)
+#define LORA_MAX_SEQS (1 << 16)
+#define LORA_MAX_FORKS 4096
+LORA_API size_t lora_cache_workspace_bytes(int n_pages, int head_dim);
+
+/*
+ * Put the keys and values of new tokens into the cache, one launch.  For each
+ * (page, k or v, head) that gets new tokens:
+ *
+ *   a      = max |x| over the page's new tokens
+ *   s      = the least power of two >= a / 448, within 2^-32 .. 2^32
+ *   page begun before (its first new place is not the page's first):
+ *   s      = max(s, its scale); its values become round(value * scale / s)
+ *   value  = round(x / s) to e4m3, ties to even, magnitudes past 448 to 448
+ *
+ * An infinity or a NaN among the new tokens makes s NaN, which turns every output
+ * that reads the page's head into NaN.  Places behind the last new token are left
+ * as they were.  The pages must be there (lora_pages_extend), and a page that gets
+ * tokens belong to one sequence alone.
+ *
+ *   k, v   device [T, ldk], [T, ldv] dtype, kv_heads heads side by side; they may
+ *          be columns of one matrix.  16-byte aligned, ldk and ldv multiples of 8.
+ */
+LORA_API lora_status lora_cache_write(lora_dtype dtype, int T, int n_seqs, int kv_heads,
+                                      int head_dim, int page_tokens, int n_pages, int max_pages,
+                                      const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                      void* cache, float* scale, const int32_t* tables,
+                                      const int32_t* lengths, const int32_t* starts, void* work,
+                                      size_t work_bytes, lora_stream_t stream);
+
+/*
+ * Attention of the new tokens over their sequences' cached ones (themselves among
+ * them: write them first).  The query at position i = length - n + its number
+ * among the sequence's n new tokens sees the positions j <= i, with window > 0
+ * only i - window < j <= i:
+ *
+ *   p_j = exp(softmax_scale q . k_j) / sum over the visible j,   y = sum_j p_j v_j
+ *
+ * with sums and softmax in fp32, q in full, the weights p rounded to 11 bits, and
+ * one rounding to dtype.  A query that sees nothing (a row of length 0, more new
+ * tokens than the length) gets zeros; the tokens of a missing page are left out.
+ * Head h reads k/v head h / (q_heads / kv_heads).
+ *
+ *   q, y     device [T, ldq], [T, ldy] dtype, q_heads heads side by side, 16-byte
+ *            aligned, strides multiples of 8; they may be columns of one matrix,
+ *            not the same ones.
+ *   softmax_scale  > 0, finite (1 / sqrt(head_dim) as a rule).
+ *   window   0: every earlier token is visible.
+ * q_heads a multiple of kv_heads, at most LORA_MAX_HEADS; T * q_heads < 2^30.
+ */
+LORA_API lora_status lora_cache_attention(lora_dtype dtype, int T, int n_seqs, int q_heads,
+                                          int kv_heads, int head_dim, int page_tokens, int n_pages,
+                                          int max_pages, const void* q, int64_t ldq,
+                                          const void* cache, const float* scale,
+                                          const int32_t* tables, const int32_t* lengths,
+                                          const int32_t* starts, float softmax_scale, int window,
+                                          void* y, int64_t ldy, void* work, size_t work_bytes,
+                                          lora_stream_t stream);
+
+/*
+ * Pages for the tokens of each sequence: the places of its table from its last
+ * held page up to ceil(lengths[b] / page_tokens) get free pages, whose count
+ * becomes 1.  Places in order of (sequence, place) take the free pages lowest
+ * first; what is not there is left -1 and counted.
+ */
+LORA_API lora_status lora_pages_extend(int n_seqs, int max_pages, int page_tokens, int n_pages,
+                                       int32_t* tables, const int32_t* lengths, int32_t* refs,
+                                       void* work, size_t work_bytes, lora_stream_t stream);
+
+/*
+ * Sequences that end: each of the n listed ones (device int32 seqs) gives its
+ * pages back (their counts go down by one), its row becomes -1 and its length 0.
+ * One that is listed twice, or holds nothing, changes nothing more.
+ */
+LORA_API lora_status lora_pages_free(int n_seqs, int max_pages, int n_pages, int32_t* tables,
+                                     int32_t* lengths, int32_t* refs, const int32_t* seqs, int n,
+                                     void* work, size_t work_bytes, lora_stream_t stream);
+
+/*
+ * Sequences that branch: for each of the n pairs (device int32 src, dst), the row
+ * dst[i], which must be empty (length 0, no page), becomes a copy of src[i].  Full
+ * pages are shared (counts up by one); the begun last page is copied, in all
+ * layers, to the lowest free page that no earlier pair took.  A source may be
+ * listed many times; of two pairs with one dst the first counts.  A pair that
+ * cannot be served (no page is free, dst holds something, src = dst, no such row)
+ * leaves dst as it was and is counted.
+ *
+ *   cache, scale   of all layers: [layers, n_pages, 2, kv_heads, page_tokens,
+ *                  head_dim] and [layers, n_pages, 2, kv_heads] contiguous.
+ *   n              at most LORA_MAX_FORKS.
+ * Two launches.
+ */
+LORA_API lora_status lora_pages_fork(int n_seqs, int max_pages, int layers, int kv_heads,
+                                     int head_dim, int page_tokens, int n_pages, int32_t* tables,
+                                     int32_t* lengths, int32_t* refs, const int32_t* src,
+                                     const int32_t* dst, int n, void* cache, float* scale,
+                                     void* work, size_t work_bytes, lora_stream_t stream);
+
+/*
+ * Move the live pages (refs > 0) together: with L of them, the k-th highest of the
+ * live pages >= L goes, in all layers, to the k-th lowest free page < L.  The
+ * tables follow; refs >= L become 0.  An entry of a page that nobody counts
+ * becomes -1 and is counted.
+ *
+ *   out_tables, out_refs   may be tables and refs (in place).
+ *   n_live                 device int32 [1], L is written; or NULL.
+ *   cache, scale           as for lora_pages_fork; pages >= L keep what they held.
+ * Two launches.
+ */
+LORA_API lora_status lora_pages_compact(int n_seqs, int max_pages, int layers, int kv_heads,
+                                        int head_dim, int page_tokens, int n_pages,
+                                        const int32_t* tables, const int32_t* refs,
+                                        int32_t* out_tables, int32_t* out_refs, int32_t* n_live,
+                                        void* cache, float* scale, void* work, size_t work_bytes,
+                                        lora_stream_t stream);
+
+/*
+ * Copy page src[i] to page dst[i] in all layers, scales with it, for the n pairs
+ * (device int32).  No page may be the target of two pairs, or target of one and
+ * source of another; a pair that names no page is left out and counted.
+ */
+LORA_API lora_status lora_pages_copy(int layers, int kv_heads, int head_dim, int page_tokens,
+                                     int n_pages, void* cache, float* scale, const int32_t* src,
+                                     const int32_t* dst, int n, void* work, size_t work_bytes,
+                                     lora_stream_t stream);
+
 /* Static, human-readable name of a status. */
 LORA_API const char* lora_status_string(lora_status status);
 
