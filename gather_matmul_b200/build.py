@@ -23,7 +23,8 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std
 
 # Compiled as whole programs: under relocatable device code ptxas ignores
 # setmaxnreg, and no device symbol of these files is used by another.
-WHOLE = {"fp8_matmul.cu", "fp8_quant.cu", "rope.cu", "cache_write.cu", "cache_pages.cu", "cache_attn.cu"}
+WHOLE = {"fp8_matmul.cu", "fp8_quant.cu", "rope.cu", "cache_write.cu", "cache_pages.cu", "cache_attn.cu",
+         "cache_attn_tc.cu"}
 
 
 def sources():

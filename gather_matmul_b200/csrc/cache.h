@@ -87,6 +87,7 @@ struct PagePlanArgs {
 
 cudaError_t launch_cache_write(lora_dtype dt, const CacheWriteArgs& a, cudaStream_t st);
 cudaError_t launch_attention_few(lora_dtype dt, const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attention_many(lora_dtype dt, const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_page_copy(const PageCopyArgs& a, cudaStream_t st);
 cudaError_t launch_pages_extend(const PagePlanArgs& a, cudaStream_t st);
 cudaError_t launch_pages_fork(const PagePlanArgs& a, cudaStream_t st);

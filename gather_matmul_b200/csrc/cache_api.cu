@@ -181,11 +181,25 @@ lora_status lora_cache_attention(lora_dtype dtype, int T, int n_seqs, int q_head
   a.P = n_pages;
   a.M = max_pages;
   a.window = window;
-  a.min_rows = 0;
-  a.max_rows = INT_MAX;
   a.c = (float)((double)softmax_scale * 1.4426950408889634);
   cudaGetLastError();
-  return from_cuda(launch_attention_few(dtype, a, (cudaStream_t)stream));
+  // Sequences of up to kFewRows rows and others go to kernels of their own.  Only
+  // the device knows them where starts is given, so both are launched then, but
+  // where all rows are few, or are those of one sequence.
+  const int rows = starts ? (int)min((int64_t)T * a.group, (int64_t)INT_MAX) : a.group;
+  const bool few = rows <= kFewRows || (starts && n_seqs > 1), many = rows > kFewRows;
+  cudaError_t e = cudaSuccess;
+  if (many) {
+    a.min_rows = few ? kFewRows + 1 : 1;
+    a.max_rows = INT_MAX;
+    e = launch_attention_many(dtype, a, (cudaStream_t)stream);
+  }
+  if (few && e == cudaSuccess) {
+    a.min_rows = 1;
+    a.max_rows = kFewRows;
+    e = launch_attention_few(dtype, a, (cudaStream_t)stream);
+  }
+  return from_cuda(e);
 }
 
 static lora_status plan_args(PagePlanArgs& a, int n_seqs, int max_pages, int page_tokens, int n_pages, void* work,

@@ -466,10 +466,11 @@ cudaError_t few_width(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// parts of the widest tile: 2 of a CTA
+// two parts of each CTA, of the kernel that needs more room
 size_t CacheWork::part_floats(int dim) {
   const int D = (dim + 63) / 64 * 64;
-  return (size_t)2 * 148 * 4 * kFewRows * (D + 2);
+  const size_t few = (size_t)148 * 4 * kFewRows, many = (size_t)148 * (D <= 128 ? kManyRows : kManyRows / 2);
+  return 2 * (few > many ? few : many) * (D + 2);
 }
 
 cudaError_t launch_attention_few(lora_dtype dt, const AttnArgs& a, cudaStream_t st) {

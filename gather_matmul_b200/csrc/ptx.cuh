@@ -424,6 +424,40 @@ __device__ __forceinline__ void tc_wait_ld32(uint32_t* r) {
 __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// 32 lanes x 16 consecutive 32-bit TMEM columns from registers; tc_wait_st waits
+// for this thread's stores.
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16: A's rows are the lanes, two
+// consecutive elements of K in each 32-bit column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      :
+      : "r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The descriptor of an operand whose N (or M) index is the contiguous one, 128-byte
+// swizzle: rows of 64 elements for one K index each, 8-row groups 1024 bytes apart
+// (bits 32-45), blocks of 64 elements of N `block_bytes` apart (bits 16-29).  The
+// instruction descriptor says so by bit 16 for B.
+__device__ __forceinline__ uint64_t umma_desc_nmajor(uint32_t smem_addr, uint32_t block_bytes) {
+  return (uint64_t)((smem_addr & 0x3FFFF) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdescNMajorB = 1u << 16;
+
 // Shared-memory matrix descriptor, K-major operand in the canonical swizzled
 // layout that a TMA copy with the same swizzle produces: rows of
 // `swizzle_bytes` bytes, 8-row groups `8 * swizzle_bytes` apart.  Fields:

@@ -626,11 +626,11 @@ def pages_extend(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor
     """Free pages, lowest first, for the places of each sequence's table that
     its length needs and that hold none yet."""
     B, M = _seqs(tables, lengths)
-    P = _list(refs, "refs")
+    P, page_tokens = _list(refs, "refs"), _int("lora_pages_extend", page_tokens)
     wp, wn = _work(work)
     st = _here(stream, tables, lengths, refs, work)
     _check("lora_pages_extend", _lib.load().lora_pages_extend(
-        B, M, _int("page_tokens", page_tokens), P, tables.data_ptr(), lengths.data_ptr(),
+        B, M, page_tokens, P, tables.data_ptr(), lengths.data_ptr(),
         refs.data_ptr(), wp, wn, st))
 
 
