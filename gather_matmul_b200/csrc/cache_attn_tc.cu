@@ -28,8 +28,14 @@ namespace {
 
 using namespace attn;
 
-constexpr int kN = 128;                       // tokens of a step (and of a unit)
-constexpr float kShift = 6.f, kSlack = 8.f;
+constexpr int kN = 128, kHalf = 64;           // tokens of a step (and of a unit), and that a softmax takes at once
+constexpr float kShift = 6.f, kMost = 32768.f;
+// A denominator below this comes from rows that see nothing: the largest weight of
+// others is at least 2^kShift / 2^32.
+constexpr float kNothing = 0x1p-60f;
+// Of each 8 pairs of weights, those whose exponentials are formed on the FMA pipe:
+// the special function unit gives 16 a cycle and SM.
+constexpr uint32_t kPolyPairs = 0x12;
 constexpr int kBlock = 4, kBlocks = 4;        // steps that are planned at once, and such blocks in shared memory
 constexpr int kRing = kBlock * kBlocks;
 
@@ -37,10 +43,14 @@ template <int D> struct Many {
   static constexpr int kTiles = D <= 128 ? 2 : 1;
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kBufs = D <= 128 ? 2 : 1;        // of k, and of v
-  // warpgroups: softmax of each tile, conversion of k, of v, products and plan; what
-  // they do with the registers that the block is launched with
+  // warpgroups: the softmax of each tile, the conversion of k, of v, products and plan
   static constexpr int kThreads = 128 * (kTiles + 3);
-  static constexpr int kSoftRegs = kTiles == 2 ? 160 : 184, kConvRegs = kTiles == 2 ? 64 : 128, kOtherRegs = kTiles == 2 ? 32 : 56;
+  // Registers of a thread at launch (checked before the first one), and the shares: the
+  // softmax takes what the others give back, no more, and those can only give.
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kSoftRegs = kTiles == 2 ? 136 : 144, kConvRegs = kTiles == 2 ? 72 : 128, kOtherRegs = kTiles == 2 ? 64 : 96;
+  static_assert(kTiles * kSoftRegs + 2 * kConvRegs + kOtherRegs <= (kTiles + 3) * kLaunchRegs, "more registers than the launch has");
+  static_assert(kSoftRegs > kLaunchRegs && kConvRegs <= kLaunchRegs && kOtherRegs < kLaunchRegs, "setmaxnreg in its direction");
   static constexpr int kTileBytes = kN * D * 2;         // 128 rows of fp16
   static constexpr int kSmem = kTileBytes * (kTiles + 2 * kBufs) + 1024;
   static constexpr int kPieces = D / 16;                // 16 bytes of e4m3 each, of a conversion thread
@@ -70,10 +80,11 @@ struct Item {
 struct ManyShared {
   Shared div;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_empty[2], plan_full[kBlocks], plan_empty[kBlocks], done;
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], o_empty[2], plan_full[kBlocks], plan_empty[kBlocks], done[2];
   uint32_t tmem;
   int stop;
   int flag[2];
+  float q_scale[2][128];                      // of a tile's rows
   Step step[kRing];
   Item item[kItems];
 };
@@ -107,6 +118,9 @@ struct Cursor {
   }
 };
 
+__device__ __forceinline__ int same(int x) { return __reduce_max_sync(~0u, x); }
+__device__ __forceinline__ uint32_t same(uint32_t x) { return __reduce_max_sync(~0u, x); }
+
 __device__ __forceinline__ uint32_t halves_lo(uint32_t two) {
   uint32_t h;
   asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(two));
@@ -122,14 +136,48 @@ __device__ __forceinline__ void fma2(float& x, float& y, uint64_t s, uint64_t l)
   asm("{\n .reg .b64 t;\n mov.b64 t, {%0, %1};\n fma.rn.f32x2 t, t, %2, %3;\n mov.b64 {%0, %1}, t;\n}"
       : "+f"(x), "+f"(y) : "l"(s), "l"(l));
 }
-__device__ __forceinline__ void add2(float& x, float& y, uint64_t l) {
-  asm("{\n .reg .b64 t;\n mov.b64 t, {%0, %1};\n add.rn.f32x2 t, t, %2;\n mov.b64 {%0, %1}, t;\n}"
-      : "+f"(x), "+f"(y) : "l"(l));
-}
 __device__ __forceinline__ uint64_t twice(float x) { return ptx::pack2(x, x); }
+// 2^x and 2^y on the FMA pipe, for arguments below 2^7: x = n + f with n the nearest
+// whole number (it is left in the low bits of x + 1.5 2^23), 2^f by the polynomial of
+// degree 4 whose relative error over |f| <= 1/2 is least (2.6e-6; fitted by
+// reweighted least squares), times 2^n made from bits.  NaN stays NaN.
+__device__ __forceinline__ void exp2_fma(float& x, float& y) {
+  constexpr float kMagic = 12582912.f;
+  uint64_t v, r, f, p;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(-126.f));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(twice(kMagic)));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(r), "l"(twice(-kMagic)));
+  f = ptx::ffma2(p, twice(-1.f), v);
+  p = ptx::ffma2(f, twice(0.009570102207362652f), twice(0.05591786280274391f));
+  p = ptx::ffma2(p, f, twice(0.240247443318367f));
+  p = ptx::ffma2(p, f, twice(0.6931217908859253f));
+  p = ptx::ffma2(p, f, twice(0.9999992847442627f));
+  const uint32_t nx = ((uint32_t)r << 23) + 0x3f800000u, ny = ((uint32_t)(r >> 32) << 23) + 0x3f800000u;
+  asm("{\n .reg .b64 n;\n mov.b64 n, {%2, %3};\n mul.rn.f32x2 n, n, %4;\n mov.b64 {%0, %1}, n;\n}"
+      : "=f"(x), "=f"(y) : "r"(nx), "r"(ny), "l"(p));
+}
 
-__device__ __forceinline__ void group_sync(int id) {
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+// 16 bytes, or zeros: no branch, so that the loads of a loop follow one another
+__device__ __forceinline__ uint4 load_if(const void* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      " @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)in));
+  return v;
+}
+// One arrival for the warp: hundreds of them a step, each a write to shared memory,
+// would be in the way of the products' operands.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(bar);
+}
+
+// the threads of a tile
+__device__ __forceinline__ void tile_sync(int tile) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + tile) : "memory");
 }
 
 // Sums of a tile's row that several CTAs share: [which][tile]: [D / 4][128] of
@@ -147,27 +195,34 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ ManyShared sm;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = ptx::smem_u32(smem), k_at = q_at + M::kTiles * M::kTileBytes, v_at = k_at + M::kBufs * M::kTileBytes;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7;
+  // Numbers that are the same in all lanes of a warp go through a warp reduction where
+  // the compiler cannot see that they are: its result is in a uniform register, and so is
+  // what follows from it (registers of the lanes are what this kernel is short of).
+  const int tid = threadIdx.x, lane = tid & 31, warp = same(tid >> 5), wg = warp >> 2;
   const uint32_t stop = ptx::smem_u32(&sm.stop);
 
   if (warp == 0) ptx::tmem_alloc(&sm.tmem, M::kCols);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.k_full[i], 128);
-      ptx::mbar_init(&sm.v_full[i], 128);
-      ptx::mbar_init(&sm.k_empty[i], 1);
-      ptx::mbar_init(&sm.v_empty[i], 1);
-      ptx::mbar_init(&sm.q_full[i], 128);
-      ptx::mbar_init(&sm.s_full[i], 1);
-      ptx::mbar_init(&sm.p_full[i], 128);
-      ptx::mbar_init(&sm.o_full[i], 1);
-      ptx::mbar_init(&sm.o_empty[i], 128);
+      ptx::mbar_init(&sm.k_full[i], 4);
+      ptx::mbar_init(&sm.v_full[i], 4);
+      ptx::mbar_init(&sm.k_empty[i], M::kTiles);
+      ptx::mbar_init(&sm.v_empty[i], M::kTiles);
+      ptx::mbar_init(&sm.q_full[i], 4);
+      ptx::mbar_init(&sm.s_full[i][0], 1);
+      ptx::mbar_init(&sm.s_full[i][1], 1);
+      ptx::mbar_init(&sm.p_full[i][0], 4);
+      ptx::mbar_init(&sm.p_full[i][1], 4);
+      ptx::mbar_init(&sm.o_full[i][0], 1);
+      ptx::mbar_init(&sm.o_full[i][1], 1);
+      ptx::mbar_init(&sm.o_empty[i], 4);
     }
     for (int i = 0; i < kBlocks; ++i) {
       ptx::mbar_init(&sm.plan_full[i], 1);
       ptx::mbar_init(&sm.plan_empty[i], 4 * (M::kTiles + 2));
     }
-    ptx::mbar_init(&sm.done, 1);
+    ptx::mbar_init(&sm.done[0], 1);
+    ptx::mbar_init(&sm.done[1], 1);
     sm.stop = 0;
     ptx::fence_mbar_init();
   }
@@ -178,8 +233,8 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
   int ctas;
   divide<M::kRows, kN>(a, sm.div, 2, w0, w1, all, ctas);   // __syncthreads
   ptx::tc_fence_after();
-  const uint32_t tmem = sm.tmem;
-  const int steps = (int)(w1 - w0);
+  const uint32_t tmem = same(sm.tmem);
+  const int steps = same((int)(w1 - w0));
   const uint32_t s_col = 0, o_col = M::kTiles * kN;
 
   if (wg < M::kTiles) {
@@ -189,7 +244,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t S = tmem + lanes + s_col + tile * kN, O = tmem + lanes + o_col + tile * D;
     float cs = 0.f;
-    int st = 0, n_s = 0, n_items = 0;
+    int st = 0, n_s = 0;
     auto planned = [&]() {
       ptx::mbar_wait_asm(ptx::smem_u32(&sm.plan_full[st / kBlock % kBlocks]), (st / kRing) & 1, stop);
     };
@@ -201,217 +256,278 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     auto seek = [&]() -> int {
       while (st < steps) {
         planned();
-        const int item = sm.step[st % kRing].item;
-        if (sm.item[item].rows > 128 * tile) return item;
-        for (int n = sm.item[item].steps; n > 0; --n) {
+        const int item = same(sm.step[st % kRing].item);
+        if (same(sm.item[item].rows) > 128 * tile) return item;
+        for (int n = same(sm.item[item].steps); n > 0; --n) {
           planned();
           pass();
         }
       }
       return -1;
     };
-    // where this thread's row of an item lies in q and y
-    auto find = [&](const Item& it, int& line, int& col) -> bool {
-      const int r = it.r0 + 128 * tile + row;
-      const bool in = 128 * tile + row < it.rows;
-      const int i = in ? r / a.group : 0;
-      line = it.q0 + i;
-      col = (it.head * a.group + (in ? r - i * a.group : 0)) * a.dim;
-      return in;
+    // Between global memory and registers a row goes through kLanes neighbouring lanes, 16
+    // bytes each: a thread for each row would touch as many lines as it has lanes.
+    constexpr int kLanes = D <= 64 ? 8 : D <= 128 ? 16 : 32, kApart = 128 / kLanes, kPasses = 128 / kApart;
+    const int tt = tid & 127, piece = tt % kLanes;
+    const int step_line = kApart / a.group, step_head = kApart % a.group;
+    // the offset of this thread's piece of a row in q or y, pass after pass, and whether
+    // there is such a row
+    struct Walk {
+      int line, head, left;
     };
-    // its q into shared memory
+    auto walk = [&](const Item& it) -> Walk {
+      const int k = 128 * tile + tt / kLanes, r = it.r0 + k;
+      return {it.q0 + r / a.group, r % a.group, 8 * piece < a.dim ? it.rows - k : 0};
+    };
+    auto place = [&](const Item& it, const Walk& w, int64_t ld) -> int64_t {
+      return (int64_t)w.line * ld + (it.head * a.group + w.head) * a.dim + 8 * piece;
+    };
+    auto on = [&](Walk& w) {
+      w.line += step_line;
+      w.head += step_head;
+      if (w.head >= a.group) w.head -= a.group, ++w.line;
+      w.left -= kApart;
+    };
+    // the tile's rows in shared memory, as the products read q; y goes through the same place
+    uint8_t* const stage = smem + (size_t)tile * M::kTileBytes;
+    auto chunk = [&](int k, int p) -> uint4* {
+      return reinterpret_cast<uint4*>(stage + (p / 8) * (kN * 128) + k * 128 + (((p & 7) ^ (k & 7)) << 4));
+    };
+    // q of the next item waits in registers, where there is room for a tile of it
+    constexpr int kGroup = kPasses <= 16 ? kPasses : 8;
+    uint4 v[kGroup];
+    Walk q_walk;
+    auto load_group = [&](const Item& it) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k, on(q_walk))
+        v[k] = load_if(static_cast<const E*>(a.q) + place(it, q_walk, a.ldq), q_walk.left > 0);
+    };
     auto load_q = [&](int item) {
-      int line, col;
-      const bool in = find(sm.item[item], line, col);
-      const E* src = static_cast<const E*>(a.q) + (int64_t)line * a.ldq + col;
-      // the row's largest element to 2^7 .. 2^8 by a power of two; read twice, 64 elements
-      // at a time, rather than held
-      float top = 0.f;
-#pragma unroll 1
-      for (int j = 0; j < D / 64; ++j) {
-        uint4 v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = in && 64 * j + 8 * e < a.dim ? ldg_nc(src + 64 * j + 8 * e) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float f[8];
-          Elem<E>::to_f32(v[e], f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-        }
+      if constexpr (kGroup == kPasses) {
+        q_walk = walk(sm.item[item]);
+        load_group(sm.item[item]);
       }
-      const int k = min(max(7 + 127 - (int)(__float_as_uint(top) >> 23), -120), 120);
-      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-      cs = __uint_as_float((uint32_t)(127 - k) << 23);
-      uint8_t* dst = smem + (size_t)tile * M::kTileBytes + row * 128;
+    };
+    auto put_q = [&](int item) {
+      if constexpr (kGroup < kPasses) q_walk = walk(sm.item[item]);
 #pragma unroll 1
-      for (int j = 0; j < D / 64; ++j) {
-        uint4 v[8];
+      for (int first = 0; first < kPasses; first += kGroup) {
+        if constexpr (kGroup < kPasses) load_group(sm.item[item]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = in && 64 * j + 8 * e < a.dim ? ldg_nc(src + 64 * j + 8 * e) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < kGroup; ++k) {
+          const int at = tt / kLanes + kApart * (first + k);
+          float f[8], top = 0.f;
+          Elem<E>::to_f32(v[k], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float f[8];
-          Elem<E>::to_f32(v[e], f);
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+          for (int d = 1; d < kLanes; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+          // the row's largest element to 2^7 .. 2^8 by a power of two
+          const int n = min(max(7 + 127 - (int)(__float_as_uint(top) >> 23), -120), 120);
+          const float up = __uint_as_float((uint32_t)(127 + n) << 23);
           uint4 w;
           w.x = Elem<__half>::pack2(f[0] * up, f[1] * up);
           w.y = Elem<__half>::pack2(f[2] * up, f[3] * up);
           w.z = Elem<__half>::pack2(f[4] * up, f[5] * up);
           w.w = Elem<__half>::pack2(f[6] * up, f[7] * up);
-          *reinterpret_cast<uint4*>(dst + j * (kN * 128) + (e ^ (row & 7)) * 16) = w;
+          if (piece < D / 8) *chunk(at, piece) = w;
+          if (piece == 0) sm.q_scale[tile][at] = __uint_as_float((uint32_t)(127 - n) << 23);
         }
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&sm.q_full[tile]);
+      tile_sync(tile);
+      cs = sm.q_scale[tile][row];
+      warp_arrive(&sm.q_full[tile], lane);
     };
     int item = seek();
-    if (item >= 0) load_q(item);
+    if (item >= 0) {
+      load_q(item);
+      put_q(item);
+    }
     while (item >= 0) {
-      int line, col, pos, from, pos_low, pos_high, tok, n_steps, first_cta, last_cta, which;
-      bool in;
+      const int now = item;
+      int pos, pos_low, pos_high, tok, n_steps;
       {
-        const Item& it = sm.item[item];
-        in = find(it, line, col);
-        pos = in ? it.base + (line - it.q0) : -1;
-        from = a.window > 0 ? pos - a.window : -1;           // visible: from < token <= pos
-        pos_low = it.base + (it.r0 + 128 * tile) / a.group;
-        pos_high = it.base + (it.r0 + min(it.rows, 128 * tile + 128) - 1) / a.group;
-        tok = it.tok;
-        n_steps = it.steps;
-        first_cta = it.first_cta;
-        last_cta = it.last_cta;
-        which = it.which;
+        const Item& it = sm.item[now];
+        pos = 128 * tile + row < it.rows ? it.base + (it.r0 + 128 * tile + row) / a.group : -1;
+        pos_low = same(it.base + (it.r0 + 128 * tile) / a.group);
+        pos_high = same(it.base + (it.r0 + min(it.rows, 128 * tile + 128) - 1) / a.group);
+        tok = same(it.tok);
+        n_steps = same(it.steps);
       }
       float m = -FLT_MAX, l = 0.f;
-      for (int i = 0; i < n_steps; ++i, tok += kN) {
-        planned();
+      for (int i = 0; i < n_steps; ++i) {
+        if (i == 0 || st % kBlock == 0) planned();
         const Step& step = sm.step[st % kRing];
-        ptx::mbar_wait_asm(ptx::smem_u32(&sm.s_full[tile]), n_s & 1, stop);
-        ++n_s;
-        ptx::tc_fence_after();
-        float x[kN];
-#pragma unroll
-        for (int j = 0; j < kN / 32; ++j) ptx::tc_ld32(S + 32 * j, reinterpret_cast<uint32_t*>(x) + 32 * j);
-#pragma unroll
-        for (int j = 0; j < kN / 32; ++j) ptx::tc_wait_ld32(reinterpret_cast<uint32_t*>(x) + 32 * j);
-        if (tok + kN - 1 > pos_low || (a.window > 0 && tok <= pos_high - a.window)) {
-          const int hi = pos - tok, lo = from - tok;                   // visible: lo < j <= hi
-#pragma unroll
-          for (int j = 0; j < kN; ++j)
-            if (j > hi || j <= lo) x[j] = -INFINITY;
-        }
-        // factors are positive: the largest score of 16 tokens gives their largest t
-        float tops[8];
-#pragma unroll
-        for (int gq = 0; gq < 8; ++gq) {
-          const float* y = x + 16 * gq;
-          float t0 = fmaxf(y[0], fmaxf(y[1], y[2])), t1 = fmaxf(y[3], fmaxf(y[4], y[5]));
-          t0 = fmaxf(t0, fmaxf(y[6], y[7]));
-          t1 = fmaxf(t1, fmaxf(y[8], y[9]));
-          t0 = fmaxf(t0, fmaxf(y[10], y[11]));
-          t1 = fmaxf(t1, fmaxf(y[12], y[13]));
-          t0 = fmaxf(t0, fmaxf(y[14], y[15]));
-          tops[gq] = fmaf(fmaxf(t0, t1), step.scale[gq].x * cs, step.scale[gq].y);
-        }
-        const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
-                                fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
-        // the products of the step before are complete: S came after them
-        if (__any_sync(~0u, top > m + kSlack)) {
-          const float n = fmaxf(m, top), f = exp2_fast(m - n);
-          m = n;
-          l *= f;
-          if (i > 0) {
+        // 64 tokens at a time: the products of one half run while the other half's weights
+        // are formed
 #pragma unroll 1
-            for (int j = 0; j < D; j += 16) {
-              uint32_t o[16];
-              ptx::tc_ld16(O + j, o);
-              ptx::tc_wait_ld16(o);
+        for (int half = 0; half < 2; ++half, tok += kHalf) {
+          const uint32_t Sh = S + kHalf * half;
+          float4 sc[4];                     // read before the wait: shared memory is busy
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              ptx::tc_st16(O + j, o);
-            }
+          for (int g = 0; g < 4; ++g) {
+            sc[g] = step.scale[4 * half + g];
+            sc[g].x *= cs;
           }
-        }
-        const float off = kShift - m;
+          ptx::mbar_wait_asm(ptx::smem_u32(&sm.s_full[tile][half]), n_s & 1, stop);
+          ptx::tc_fence_after();
+          const bool edge = tok + kHalf - 1 > pos_low || (a.window > 0 && tok <= pos_high - a.window);
+          // 32 scores, asked for and taken
+          auto ask = [&](int j, float* x) { ptx::tc_ld32(Sh + j, reinterpret_cast<uint32_t*>(x)); };
+          auto take = [&](int j, float* x) {
+            ptx::tc_wait_ld32(reinterpret_cast<uint32_t*>(x));
+            if (edge) {
+              const int hi = pos - (tok + j), lo = a.window > 0 ? hi - a.window : -1;   // visible: lo < e <= hi
 #pragma unroll
-        for (int gq = 0; gq < 8; gq += 2) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float* y = x + 16 * (gq + e);
-            const float4 sc = step.scale[gq + e];
-            const uint64_t s2 = twice(sc.x * cs), l2 = twice(sc.y + off);
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) fma2(y[j], y[j + 1], s2, l2);
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              y[j] = exp2_fast(y[j]);
-              y[j + 1] = exp2_fast(y[j + 1]);
-              add2(s0, s1, ptx::pack2(y[j], y[j + 1]));
-              p[8 * e + j / 2] = Elem<__half>::pack2(y[j], y[j + 1]);
+              for (int e = 0; e < 32; ++e)
+                if (e > hi || e <= lo) x[e] = -INFINITY;
             }
-            l = fmaf(s0 + s1, sc.z, l);
+          };
+          auto raise = [&]() {
+            float top = m;
+#pragma unroll 1
+            for (int j = 0; j < kHalf; j += 32) {
+              float x[32];
+              ask(j, x);
+              take(j, x);
+#pragma unroll
+              for (int e = 0; e < 32; e += 16) {
+                // factors are positive: the largest score of 16 tokens gives their largest t
+                float t = x[e];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) t = fmaxf(t, x[e + i]);
+                const float4 s4 = step.scale[4 * half + (j + e) / 16];
+                top = fmaxf(top, fmaf(t, s4.x * cs, s4.y));
+              }
+            }
+            const float f = exp2_fast(m - top);
+            m = top;
+            l *= f;
+            if (i > 0 || half > 0) {
+              // once the products of all weights so far are in
+              ptx::mbar_wait_asm(ptx::smem_u32(&sm.o_full[tile][half ^ 1]), (n_s + half + 1) & 1, stop);
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int j = 0; j < D; j += 16) {
+                uint32_t o[16];
+                ptx::tc_ld16(O + j, o);
+                ptx::tc_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                ptx::tc_st16(O + j, o);
+              }
+            }
+          };
+          // The weights of an item's first tokens need their maximum.  Later ones are formed
+          // with the maximum so far, and again with the new one where they show to be too
+          // large for fp16: where the sum of 16 of them passes kMost.
+          if (i == 0 && half == 0) raise();
+          uint32_t p[kHalf / 2];
+          for (int again = 0;; ++again) {
+            const float off = kShift - m;
+            float sum = 0.f, most = 0.f, x[2][32];
+            ask(0, x[0]);
+#pragma unroll
+            for (int h = 0; h < kHalf; h += 16) {
+              float* y = x[h / 32 & 1] - h / 32 * 32;
+              if (h % 32 == 0) {
+                take(h, y + h);
+                if (h + 32 < kHalf) ask(h + 32, x[(h / 32 + 1) & 1]);
+              }
+              const uint64_t s2 = twice(sc[h / 16].x), l2 = twice(sc[h / 16].y + off);
+              float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+              for (int e = h; e < h + 16; e += 2) {
+                fma2(y[e], y[e + 1], s2, l2);
+                if ((kPolyPairs >> (e / 2 % 8)) & 1) {
+                  exp2_fma(y[e], y[e + 1]);
+                } else {
+                  y[e] = exp2_fast(y[e]);
+                  y[e + 1] = exp2_fast(y[e + 1]);
+                }
+                s0 += y[e];
+                s1 += y[e + 1];
+                p[e / 2] = Elem<__half>::pack2(y[e], y[e + 1]);
+              }
+              s0 += s1;
+              most = fmaxf(most, s0);
+              sum = fmaf(s0, sc[h / 16].z, sum);
+            }
+            if (!__any_sync(~0u, most > kMost) || again) {   // with a new maximum none is too large
+              l += sum;
+              break;
+            }
+            raise();
           }
-          ptx::tc_st16(S + 8 * gq, p);
+#pragma unroll
+          for (int j = 0; j < kHalf / 2; j += 16) ptx::tc_st16(Sh + j, p + j);
+          ptx::tc_wait_st();
+          ptx::tc_fence_before();
+          warp_arrive(&sm.p_full[tile][half], lane);
         }
-        ptx::tc_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&sm.p_full[tile]);
+        ++n_s;
         pass();
       }
-      // q of the next item, while this one's last products run
+      // q of the next item into registers, while this one's last products run
       item = seek();
       if (item >= 0) load_q(item);
-      ptx::mbar_wait_asm(ptx::smem_u32(&sm.o_full[tile]), n_items & 1, stop);
-      ++n_items;
+      ptx::mbar_wait_asm(ptx::smem_u32(&sm.o_full[tile][1]), (n_s + 1) & 1, stop);   // the last half's products
       ptx::tc_fence_after();
-      E* out = static_cast<E*>(a.y) + (int64_t)line * a.ldy + col;
+      // the thread's row, into the place of q
+      const Item& it = sm.item[now];
+      const int which = same(it.which);
+      auto put = [&](int j, const float* o) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          uint4 w;
+          w.x = Elem<E>::pack2(o[e], o[e + 1]);
+          w.y = Elem<E>::pack2(o[e + 2], o[e + 3]);
+          w.z = Elem<E>::pack2(o[e + 4], o[e + 5]);
+          w.w = Elem<E>::pack2(o[e + 6], o[e + 7]);
+          *chunk(row, (j + e) / 8) = w;
+        }
+      };
+      bool out = which < 0;
       if (which < 0) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l < kNothing ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int j = 0; j < D; j += 16) {
+          float o[16];
+          ptx::tc_ld16(O + j, reinterpret_cast<uint32_t*>(o));
+          ptx::tc_wait_ld16(reinterpret_cast<uint32_t*>(o));
 #pragma unroll
-        for (int j = 0; j < D; j += 32) {
-          float o[32];
-          ptx::tc_ld32(O + j, reinterpret_cast<uint32_t*>(o));
-          ptx::tc_wait_ld32(reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (in && j + e < a.dim) {
-              uint4 v;
-              v.x = Elem<E>::pack2(o[e] * inv, o[e + 1] * inv);
-              v.y = Elem<E>::pack2(o[e + 2] * inv, o[e + 3] * inv);
-              v.z = Elem<E>::pack2(o[e + 4] * inv, o[e + 5] * inv);
-              v.w = Elem<E>::pack2(o[e + 6] * inv, o[e + 7] * inv);
-              *reinterpret_cast<uint4*>(out + j + e) = v;
-            }
-          }
+          for (int e = 0; e < 16; ++e) o[e] *= inv;
+          put(j, o);
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&sm.o_empty[tile]);
+        warp_arrive(&sm.o_empty[tile], lane);
       } else {
+        const int first_cta = same(it.first_cta), last_cta = same(it.last_cta);
         float* part = part_of<D>(a, blockIdx.x, which, tile);
+#pragma unroll 1
+        for (int j = 0; j < D; j += 16) {
+          float o[16];
+          ptx::tc_ld16(O + j, reinterpret_cast<uint32_t*>(o));
+          ptx::tc_wait_ld16(reinterpret_cast<uint32_t*>(o));
 #pragma unroll
-        for (int j = 0; j < D; j += 32) {
-          float o[32];
-          ptx::tc_ld32(O + j, reinterpret_cast<uint32_t*>(o));
-          ptx::tc_wait_ld32(reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
+          for (int e = 0; e < 16; e += 4)
             __stcg(reinterpret_cast<float4*>(part) + (size_t)((j + e) / 4) * 128 + row,
                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
         }
         __stcg(reinterpret_cast<float2*>(part + 128 * D) + row, make_float2(m, l));
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&sm.o_empty[tile]);
+        warp_arrive(&sm.o_empty[tile], lane);
         __threadfence();
-        group_sync(1 + tile);
+        tile_sync(tile);
         if (row == 0) {
           int* join = a.join + 2 * first_cta + tile;
           sm.flag[tile] = atomicAdd(join, 1) == last_cta - first_cta;
           if (sm.flag[tile]) *join = 0;                   // as the next call finds it
         }
-        group_sync(1 + tile);
-        if (sm.flag[tile]) {
+        tile_sync(tile);
+        out = same(sm.flag[tile]);
+        if (out) {
           __threadfence();
           float top = -FLT_MAX, sum = 0.f;
           for (int k = first_cta; k <= last_cta; ++k) {
@@ -420,39 +536,39 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
             sum = sum * exp2_fast(top - up) + ms.y * exp2_fast(ms.x - up);
             top = up;
           }
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          for (int j = 0; j < a.dim; j += 16) {
+          const float inv = sum < kNothing ? 0.f : 1.f / sum;
+#pragma unroll 1
+          for (int j = 0; j < D; j += 16) {
             float o[16] = {};
             for (int k = first_cta; k <= last_cta; ++k) {
               const float* pk = part_of<D>(a, k, k == first_cta ? 1 : 0, tile);
               const float f = exp2_fast(__ldcg(reinterpret_cast<const float2*>(pk + 128 * D) + row).x - top) * inv;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(pk) + (size_t)(j / 4 + e) * 128 + row);
-                o[4 * e] = fmaf(v.x, f, o[4 * e]);
-                o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
-                o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
-                o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
+              for (int e = 0; e < 16; e += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(pk) + (size_t)((j + e) / 4) * 128 + row);
+                o[e] = fmaf(x.x, f, o[e]);
+                o[e + 1] = fmaf(x.y, f, o[e + 1]);
+                o[e + 2] = fmaf(x.z, f, o[e + 2]);
+                o[e + 3] = fmaf(x.w, f, o[e + 3]);
               }
             }
-            if (in) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 8) {
-                uint4 v;
-                v.x = Elem<E>::pack2(o[e], o[e + 1]);
-                v.y = Elem<E>::pack2(o[e + 2], o[e + 3]);
-                v.z = Elem<E>::pack2(o[e + 4], o[e + 5]);
-                v.w = Elem<E>::pack2(o[e + 6], o[e + 7]);
-                *reinterpret_cast<uint4*>(out + j + e) = v;
-              }
-            }
+            put(j, o);
           }
         }
       }
+      if (out) {
+        tile_sync(tile);
+        Walk w = walk(it);
+#pragma unroll 1
+        for (int k = tt / kLanes; k < 128 && w.left > 0; k += kApart, on(w))
+          *reinterpret_cast<uint4*>(static_cast<E*>(a.y) + place(it, w, a.ldy)) = *chunk(k, piece);
+        tile_sync(tile);
+      }
+      if (item >= 0) put_q(item);
     }
   } else if (wg < M::kTiles + 2) {
     // ------------------------------------------------------------ conversion
-    ptx::reg_dec<M::kConvRegs>();
+    if constexpr (M::kConvRegs < M::kLaunchRegs) ptx::reg_dec<M::kConvRegs>();
     const int ct = tid & 127;
     const bool is_v = wg == M::kTiles + 1;
     const int64_t side = is_v ? ((int64_t)a.Hk * a.dim) << a.page_log : 0;
@@ -460,24 +576,26 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     const uint32_t tiles_at = is_v ? v_at : k_at;
     uint64_t *const full = is_v ? sm.v_full : sm.k_full, *const empty = is_v ? sm.v_empty : sm.k_empty;
     uint4 r[M::kPieces];
-    // A thread's pieces of 16 bytes: four lanes take 64 bytes of a row, the next four
-    // of the row behind it, so that the halves they store hit different banks.
-    auto place = [&](int k, int& row, int& e) {
-      const int i = ct + 128 * k, rest = i >> 3;
-      e = 64 * (rest % (D / 64)) + 16 * (i & 3);
-      row = 2 * (rest / (D / 64)) + ((i >> 2) & 1);
-    };
+    // A thread's pieces of 16 bytes: the same 16 of each 64-byte column, of every 32nd
+    // row.  Four lanes take 64 bytes of a row, the next four of the row behind it, so that
+    // the halves they store hit different banks; what depends on the lane is the same for
+    // all pieces, the rest is known to the compiler.
+    constexpr int A = D / 64;
+    const int row0 = 2 * (ct >> 3) + ((ct >> 2) & 1), e0 = 16 * (ct & 3);
+    const int64_t lane_at = (row0 & 15) * a.dim + e0;
+    const uint32_t lane_sm = row0 * 128 + (((2 * (ct & 3)) ^ (row0 & 7)) << 4);
     auto load = [&](int st) {
-      ptx::mbar_wait_asm(ptx::smem_u32(&sm.plan_full[st / kBlock % kBlocks]), (st / kRing) & 1, stop);
+      if (st % kBlock == 0)
+        ptx::mbar_wait_asm(ptx::smem_u32(&sm.plan_full[st / kBlock % kBlocks]), (st / kRing) & 1, stop);
       const Step& step = sm.step[st % kRing];
       const int visible = is_v ? step.visible : kN;         // v behind the last visible token may be
 #pragma unroll                                              // anything: zeros in its place
-      for (int k = 0; k < M::kPieces; ++k) {
-        int row, e;
-        place(k, row, e);
-        const int64_t at = step.at[row >> 4];
-        r[k] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && e < a.dim && row < visible) r[k] = ldg_stream(base + at + (row & 15) * a.dim + e);
+      for (int g = 0; g < 4; ++g) {
+        const int64_t at = step.at[2 * g + (row0 >> 4)];
+        const uint8_t* src = base + at + lane_at;
+        const bool in = at >= 0 && row0 + 32 * g < visible;
+#pragma unroll
+        for (int c = 0; c < A; ++c) r[g * A + c] = load_if(src + 64 * c, in && e0 + 64 * c < a.dim);
       }
       // this step's entries are not looked at again
       if (st % kBlock == kBlock - 1) {
@@ -489,77 +607,73 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     for (int st = 0; st < steps; ++st) {
       const int buf = st % M::kBufs, use = st / M::kBufs;
       if (use > 0) ptx::mbar_wait_asm(ptx::smem_u32(&empty[buf]), (use - 1) & 1, stop);
-      const uint32_t dst = tiles_at + buf * M::kTileBytes;
+      const uint32_t dst = tiles_at + buf * M::kTileBytes + lane_sm, dst2 = dst ^ 16;
 #pragma unroll
       for (int k = 0; k < M::kPieces; ++k) {
-        int row, e;
-        place(k, row, e);
-        const uint32_t at = dst + (e / 64) * (kN * 128) + row * 128, c0 = ((e & 63) >> 3) ^ (row & 7);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (c0 << 4)), "r"(halves_lo(r[k].x)), "r"(halves_hi(r[k].x)),
+        const uint32_t at = (k % A) * (kN * 128) + (k / A) * (32 * 128);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at), "r"(halves_lo(r[k].x)), "r"(halves_hi(r[k].x)),
                      "r"(halves_lo(r[k].y)), "r"(halves_hi(r[k].y)) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((c0 ^ 1) << 4)), "r"(halves_lo(r[k].z)), "r"(halves_hi(r[k].z)),
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst2 + at), "r"(halves_lo(r[k].z)), "r"(halves_hi(r[k].z)),
                      "r"(halves_lo(r[k].w)), "r"(halves_hi(r[k].w)) : "memory");
       }
+      ptx::fence_proxy_async_smem();        // before the next loads: it would wait for them
+      warp_arrive(&full[buf], lane);
       if (st + 1 < steps) load(st + 1);
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(&full[buf]);
     }
   } else {
     // ------------------------------------------------------------ products
     ptx::reg_dec<M::kOtherRegs>();
-    if (warp == 4 * (M::kTiles + 2)) {
-      // Whatever an instruction's operands or the loop depend on goes through a warp
-      // reduction, whose result the compiler knows to be the same in all lanes: it
-      // keeps it in uniform registers, as these instructions want it (moving it there
-      // for each one made an issue of 16 take 1050 cycles).
+    const int role = warp - 4 * (M::kTiles + 2);
+    // One warp issues a tile's products, so that one waits while the other's run.
+    auto issue = [&](auto tile) {
+      constexpr int t = decltype(tile)::value;
+      // operands of these instructions are wanted in uniform registers; moving them there
+      // for each one made an issue of 16 take 1050 cycles
       const bool one = ptx::elect_one();
-      const uint32_t tm = __reduce_or_sync(~0u, tmem);
-      const int n_steps = (int)__reduce_max_sync(~0u, (unsigned)steps);
-      constexpr uint32_t id_s = ptx::umma_idesc_f16(false, 128, kN);
+      constexpr uint32_t id_s = ptx::umma_idesc_f16(false, 128, kHalf);
       constexpr uint32_t id_o = ptx::umma_idesc_f16(false, 128, D) | ptx::kIdescNMajorB;
       const uint64_t q_desc = ptx::umma_desc_kmajor(q_at, 128), k_desc = ptx::umma_desc_kmajor(k_at, 128);
       const uint64_t v_desc = ptx::umma_desc_nmajor(v_at, kN * 128);
       constexpr uint64_t kTile16 = M::kTileBytes >> 4;
-      uint32_t n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0, n_o0 = 0, n_o1 = 0;
+      uint32_t n_q = 0, n_p = 0, n_o = 0;
       auto flags = [&](int st) -> uint32_t {
         ptx::mbar_wait_asm(ptx::smem_u32(&sm.k_full[st % M::kBufs]), (st / M::kBufs) & 1, stop);
-        return __reduce_or_sync(~0u, sm.step[st % kRing].flags);
+        return same(sm.step[st % kRing].flags);
       };
-      auto scores = [&](auto tile, int st, uint32_t f) {
-        constexpr int t = decltype(tile)::value;
-        uint32_t& n_q = t ? n_q1 : n_q0;
-        if (f & kFirst) {
+      auto scores = [&](auto half, int st, uint32_t f) {
+        constexpr int h = decltype(half)::value;
+        if (h == 0 && (f & kFirst)) {
           ptx::mbar_wait_asm(ptx::smem_u32(&sm.q_full[t]), n_q & 1, stop);
           ++n_q;
         }
         ptx::tc_fence_after();
         if (one) {
-          const uint64_t k = k_desc + (uint32_t)(st % M::kBufs) * kTile16;
+          const uint64_t k = k_desc + (uint32_t)(st % M::kBufs) * kTile16 + h * (kHalf * 128 >> 4);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             const uint32_t off = ((j / 4) * (kN * 128) + (j % 4) * 32) >> 4;
-            ptx::tc_mma_f16(tm + s_col + t * kN, q_desc + t * kTile16 + off, k + off, id_s, j > 0);
+            ptx::tc_mma_f16(tmem + s_col + t * kN + h * kHalf, q_desc + t * kTile16 + off, k + off, id_s, j > 0);
           }
-          ptx::tc_commit(&sm.s_full[t]);
+          ptx::tc_commit(&sm.s_full[t][h]);
         }
         __syncwarp();
       };
-      auto sums = [&](auto tile, int st, uint32_t f) {
-        constexpr int t = decltype(tile)::value;
-        uint32_t &n_p = t ? n_p1 : n_p0, &n_o = t ? n_o1 : n_o0;
-        ptx::mbar_wait_asm(ptx::smem_u32(&sm.p_full[t]), n_p & 1, stop);
-        ++n_p;
-        if (f & kFirst) {
+      auto sums = [&](auto half, int st, uint32_t f) {
+        constexpr int h = decltype(half)::value;
+        ptx::mbar_wait_asm(ptx::smem_u32(&sm.p_full[t][h]), n_p & 1, stop);
+        if (h == 1) ++n_p;
+        if (h == 0 && (f & kFirst)) {
           if (n_o > 0) ptx::mbar_wait_asm(ptx::smem_u32(&sm.o_empty[t]), (n_o - 1) & 1, stop);
           ++n_o;
         }
         ptx::tc_fence_after();
         if (one) {
-          const uint64_t v = v_desc + (uint32_t)(st % M::kBufs) * kTile16;
+          const uint64_t v = v_desc + (uint32_t)(st % M::kBufs) * kTile16 + h * (kHalf * 128 >> 4);
 #pragma unroll
-          for (int j = 0; j < kN / 16; ++j)
-            ptx::tc_mma_f16_ts(tm + o_col + t * D, tm + s_col + t * kN + 8 * j, v + j * (2048 >> 4), id_o, j > 0 || !(f & kFirst));
-          if (f & kLast) ptx::tc_commit(&sm.o_full[t]);
+          for (int j = 0; j < kHalf / 16; ++j)
+            ptx::tc_mma_f16_ts(tmem + o_col + t * D, tmem + s_col + t * kN + h * kHalf + 8 * j, v + j * (2048 >> 4), id_o,
+                               h > 0 || j > 0 || !(f & kFirst));
+          ptx::tc_commit(&sm.o_full[t][h]);
         }
         __syncwarp();
       };
@@ -567,45 +681,58 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
         if (one) ptx::tc_commit(bar);
         __syncwarp();
       };
-      constexpr std::integral_constant<int, 0> t0{};
-      constexpr std::integral_constant<int, M::kTiles - 1> t1{};
+      constexpr std::integral_constant<int, 0> h0{};
+      constexpr std::integral_constant<int, 1> h1{};
+      // a step in which the tile has no rows: its buffer's use is over for this warp
+      auto skip = [&](uint64_t* bar) {
+        if (one) ptx::mbar_arrive(bar);
+        __syncwarp();
+      };
+      const uint32_t mine = t == 0 ? 0 : kSecond;               // the flag of items with rows for this tile
+      auto all_scores = [&](int st, uint32_t f) {
+        uint64_t* bar = &sm.k_empty[st % M::kBufs];
+        if ((f & mine) != mine) return skip(bar);
+        scores(h0, st, f);
+        scores(h1, st, f);
+        commit(bar);
+      };
       uint32_t now = 0;
-      if (n_steps > 0) {
+      if (steps > 0) {
         now = flags(0);
-        scores(t0, 0, now);
-        if (now & kSecond) scores(t1, 0, now);
-        commit(&sm.k_empty[0]);
+        all_scores(0, now);
       }
-      for (int st = 0; st < n_steps; ++st) {
+      for (int st = 0; st < steps; ++st) {
         const int buf = st % M::kBufs;
-        const bool go_on = st + 1 < n_steps;
+        const bool go_on = st + 1 < steps;
         const uint32_t then = go_on ? flags(st + 1) : 0;
         ptx::mbar_wait_asm(ptx::smem_u32(&sm.v_full[buf]), (st / M::kBufs) & 1, stop);
-        if (!(now & kLast)) {
-          sums(t0, st, now);
-          scores(t0, st + 1, then);
-          if (now & kSecond) {
-            sums(t1, st, now);
-            scores(t1, st + 1, then);
-          }
+        if ((now & mine) != mine) {
+          skip(&sm.v_empty[buf]);
+          if (go_on) all_scores(st + 1, then);
+        } else if (!(now & kLast)) {
+          // within an item each half's scores of the next step follow its sums of this one
+          sums(h0, st, now);
+          scores(h0, st + 1, then);
+          sums(h1, st, now);
+          scores(h1, st + 1, then);
           commit(&sm.v_empty[buf]);
           commit(&sm.k_empty[(st + 1) % M::kBufs]);
         } else {
-          sums(t0, st, now);
-          if (now & kSecond) sums(t1, st, now);
+          sums(h0, st, now);
+          sums(h1, st, now);
           commit(&sm.v_empty[buf]);
-          if (go_on) {
-            scores(t0, st + 1, then);
-            if (then & kSecond) scores(t1, st + 1, then);
-            commit(&sm.k_empty[(st + 1) % M::kBufs]);
-          }
+          if (go_on) all_scores(st + 1, then);
         }
         now = then;
       }
       // nothing is in flight when tensor memory goes back
-      commit(&sm.done);
-      ptx::mbar_wait_asm(ptx::smem_u32(&sm.done), 0, stop);
-    } else if (warp == 4 * (M::kTiles + 2) + 1) {
+      commit(&sm.done[t]);
+      ptx::mbar_wait_asm(ptx::smem_u32(&sm.done[t]), 0, stop);
+    };
+    if (role < M::kTiles) {
+      if (role == 0) issue(std::integral_constant<int, 0>{});
+      else issue(std::integral_constant<int, M::kTiles - 1>{});
+    } else if (role == M::kTiles) {
       // ---------------------------------------------------------- plan
       // four steps at a time, eight lanes for the groups of each
       const int64_t head_bytes = (int64_t)a.dim << a.page_log;
@@ -696,7 +823,11 @@ cudaError_t many_launch(const AttnArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(attention_many_kernel<D, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSmem);
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, attention_many_kernel<D, E>);
+    if (e == cudaSuccess && f.numRegs != M::kLaunchRegs) e = cudaErrorInvalidConfiguration;   // the shares would not fit
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attention_many_kernel<D, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }

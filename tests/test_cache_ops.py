@@ -10,8 +10,9 @@ Tolerances, from the arithmetic (u = half a step of the output's type, relative:
   attention   a logit is a sum of dim products in fp32, each step off by at most
               2^-23 (truncated): (dim + 8) 2^-23 c sum |q k|, and three roundings
               of it and of the running maximum, 2^-22 of the largest magnitude
-              each in units of its logarithm; 2^-22 for the exponential.  Call
-              the sum of these e: a weight is off by the factor 1 +- 2 e, numerator and
+              each in units of its logarithm; 2^-18 for the exponential (the
+              polynomial that some are formed by is off by 2.6e-6).  Call the
+              sum of these e: a weight is off by the factor 1 +- 2 e, numerator and
               denominator alike, so 4 e covers their quotient.  Weights round to
               fp16, 2^-11, or by 2^-25 absolutely where they are small: the
               largest weight is at least 2^6, so 2^-31 of it each.  The sums over
@@ -122,7 +123,7 @@ def check_attention(c, q, y, news, softmax_scale=None, window=0):
             ref, mag = p @ v, p @ v.abs()
             big = ((qq.abs() @ k.abs().t()) * sm).masked_fill(~seen, 0.0).amax(1, keepdim=True)
             logs = (big + 40) * 2.0 ** -22
-            e = (c.dim + 8) * 2.0 ** -23 * big + 3 * logs + 2.0 ** -22
+            e = (c.dim + 8) * 2.0 ** -23 * big + 3 * logs + 2.0 ** -18
             tol = mag * (4 * e + 2.0 ** -11 + (length / 8 + 64) * 2.0 ** -23) + \
                 length * 2.0 ** -31 * v.abs().max() + U[y.dtype] * 1.001 * ref.abs() + 2.0 ** -25
             err = (got.double() - ref).abs()
