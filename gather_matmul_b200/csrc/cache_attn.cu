@@ -31,22 +31,41 @@ using namespace attn;
 
 constexpr int kFThreads = 128, kFWarps = 4;
 constexpr int kFUnit = 64;                  // tokens of a unit: 16 for each warp
+constexpr int kIdle = 2;                    // what an item costs beside its tokens, in units
 constexpr float kShift = 6.f, kSlack = 8.f;
 
-template <int D> struct FewShape;           // stages, and CTAs that share an SM
-template <> struct FewShape<64> { static constexpr int kStages = 6; };
-template <> struct FewShape<128> { static constexpr int kStages = 3; };
-template <> struct FewShape<192> { static constexpr int kStages = 3; };
-template <> struct FewShape<256> { static constexpr int kStages = 3; };
+// Groups of 16 tokens that a warp has in registers, and CTAs that share an SM.
+template <int D, int NT> struct FewShape {
+  static constexpr int kBufs = 1;
+  static constexpr int kCtas = D <= 128 ? (NT == 1 ? 4 : 3) : 2;
+};
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// 16 or 8 bytes, or zeros; no branch, so that loads follow one another
+__device__ __forceinline__ uint4 load16(const void* p, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      " @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)in));
+  return v;
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+__device__ __forceinline__ uint2 load8(const void* p, bool in) {
+  uint2 v;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %3, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n"
+      " @p ld.global.nc.v2.u32 {%0, %1}, [%2];\n}"
+      : "=&r"(v.x), "=&r"(v.y) : "l"(p), "r"((uint32_t)in));
+  return v;
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // two e4m3 codes (low byte first) to two halves
 __device__ __forceinline__ uint32_t halves(uint32_t two) {
@@ -80,17 +99,14 @@ __device__ __forceinline__ void put_row(const AttnArgs& a, const Tile& t, int h,
 }
 
 template <int D, int NT, typename E>
-__global__ void __launch_bounds__(kFThreads, D <= 128 ? (NT == 1 ? 4 : 3) : 2)
+__global__ void __launch_bounds__(kFThreads, FewShape<D, NT>::kCtas)
 attention_few_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int R = 8 * NT, ST = FewShape<D>::kStages;
-  constexpr int KP = D / 32;               // 16-byte pieces of k that a thread holds: 2 tokens, D / 4 each
-  constexpr int KT = D / 64;               //   of one token
+  constexpr int R = 8 * NT, BUFS = FewShape<D, NT>::kBufs;
+  constexpr int KT = D / 64;               // 16-byte pieces of k of a token that a thread holds (of 2 tokens)
   constexpr int MT = D / 16;               // m-tiles of the v product, and words of k of a token
   constexpr int VB = D / 8;                // bytes of v of one token (4 tokens)
-  constexpr int NP = D / 16;               // 16-byte pieces in all
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
-  __shared__ float2 scales[ST][kFWarps];
   __shared__ float stat[kFWarps][R][2];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
@@ -98,7 +114,7 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
 
   unsigned long long w0, w1, all;
   int ctas;
-  divide<R, kFUnit>(a, sh, 2, w0, w1, all, ctas);
+  divide<R, kFUnit, kIdle>(a, sh, 2, w0, w1, all, ctas);
   if (w0 >= w1) return;
   int64_t slot = sh.slot;
   int seq = sh.seq;
@@ -109,16 +125,22 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
   while (w < w1) {
     Tile t;
     while (seq + 1 < a.B && slot_of<R>(a, seq + 1) <= slot) ++seq;
-    tile_of<R, kFUnit>(a, seq, slot, t);
+    tile_of<R, kFUnit, kIdle>(a, seq, slot, t);
     const unsigned long long slot_units = (unsigned long long)t.units * a.Hk;
     if (off >= slot_units) {                // this slot is done (or holds no rows)
       off -= slot_units;
       ++slot;
       continue;
     }
-    const int h = (int)(off / t.units), ua = (int)(off - (unsigned long long)h * t.units);
-    const int nu = (int)min((unsigned long long)(t.units - ua), w1 - w);
-    const unsigned long long item0 = w - ua, item1 = item0 + t.units;
+    const int h = (int)(off / t.units), from = (int)(off - (unsigned long long)h * t.units);
+    const int share = (int)min((unsigned long long)(t.units - from), w1 - w);
+    // of the units that have tokens
+    const int ua = max(from - kIdle, 0), nu = from + share - kIdle - ua;
+    const unsigned long long item0 = w - from + kIdle, item1 = w - from + t.units;
+    const bool begins = from <= kIdle;
+    w += share;
+    off += share;
+    if (nu <= 0) continue;
 
     // ---- copies: iteration it of this warp takes tokens tok0 + it * kFUnit .. + 16
     const int tok0 = (t.u0 + ua) * kFUnit + warp * 16;
@@ -136,51 +158,58 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
     };
-    unsigned ready = 0;                     // bit s: stage s holds tokens
-    auto issue = [&](int it) {
+    // A group in registers: k of tokens g and g + 8, elements from c D / 4 on; v of tokens
+    // 2c, 2c + 1, 2c + 8, 2c + 9, elements from g D / 8 on; the scales.
+    struct Group {
+      uint4 k[2 * KT];
+      uint32_t v[4][VB / 4];
+      float ks, vs;
+      const uint8_t* at;                    // its k in the cache, or null
+    };
+    const int k_lane = g * a.dim + c * (D / 4), v_lane = 2 * c * a.dim + g * VB;
+    auto load_k = [&](Group& r, int it) {
       if ((it & 31) == 0) fetch_pids(it);
-      const int s = it % ST;
       const int pid = __shfl_sync(~0u, pids, it & 31);
-      ready &= ~(1u << s);
-      if (it < nu && pid >= 0) {
-        ready |= 1u << s;
-        const int tok = tok0 + it * kFUnit, in_page = tok & (page - 1);
-        const uint8_t* k = base + (int64_t)pid * page_bytes + (int64_t)in_page * a.dim;
-        const uint8_t* v = k + v_off;
-        const uint32_t dst = ptx::smem_u32(smem) + (uint32_t)(s * NP * kFThreads + tid) * 16;
+      const bool in = it < nu && pid >= 0;
+      const int tok = tok0 + it * kFUnit;
+      r.at = in ? base + (int64_t)pid * page_bytes + (int64_t)(tok & (page - 1)) * a.dim : nullptr;
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {      // tokens g and g + 8, elements from c D / 4 on
-          const int e = c * (D / 4) + 16 * (i % KT);
-          copy16(dst + (uint32_t)i * kFThreads * 16, k + (int64_t)(g + 8 * (i / KT)) * a.dim + (e < a.dim ? e : 0), e < a.dim);
-        }
-        const uint32_t vd = ptx::smem_u32(smem) + (uint32_t)(s * NP + KP) * kFThreads * 16;
+      for (int j = 0; j < KT; ++j) {
+        const bool ok = in && c * (D / 4) + 16 * j < a.dim;
+        r.k[j] = load16(r.at + k_lane + 16 * j, ok);
+        r.k[KT + j] = load16(r.at + k_lane + 8 * a.dim + 16 * j, ok);
+      }
+      r.ks = r.vs = 1.f;
+      if (in) {
+        const float* sp = a.scale + (int64_t)pid * 2 * a.Hk + h;
+        r.ks = __ldg(sp);
+        r.vs = __ldg(sp + a.Hk);
+      }
+    };
+    auto load_v = [&](Group& r, int it) {
+      const uint8_t* v = r.at + v_off + v_lane;
+      const int left = r.at ? t.hi - (tok0 + it * kFUnit) - 2 * c : 0;   // what lies behind may be anything: zeros in its place
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {       // tokens 2c, 2c + 1, 2c + 8, 2c + 9, elements from g D / 8 on
-          const int tk = 2 * c + (i & 1) + 8 * (i >> 1);
-          const bool in = tok + tk < t.hi;  // what lies behind may be anything: zeros in its place
-          if constexpr (VB % 16 == 0) {
+      for (int i = 0; i < 4; ++i) {
+        const int tk = (i & 1) + 8 * (i >> 1);
+        if constexpr (VB % 16 == 0) {
 #pragma unroll
-            for (int j = 0; j < VB / 16; ++j) {
-              const int e = g * VB + 16 * j;
-              const bool ok = in && e < a.dim;
-              copy16(vd + (uint32_t)((i * (VB / 16) + j) * kFThreads + tid) * 16, v + (ok ? (int64_t)tk * a.dim + e : 0), ok);
-            }
-          } else {
+          for (int j = 0; j < VB / 16; ++j) {
+            const uint4 x = load16(v + tk * a.dim + 16 * j, tk < left && g * VB + 16 * j < a.dim);
+            r.v[i][4 * j] = x.x, r.v[i][4 * j + 1] = x.y, r.v[i][4 * j + 2] = x.z, r.v[i][4 * j + 3] = x.w;
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < VB / 8; ++j) {
-              const int e = g * VB + 8 * j;
-              const bool ok = in && e < a.dim;
-              copy8(vd + (uint32_t)((i * (VB / 8) + j) * kFThreads + tid) * 8, v + (ok ? (int64_t)tk * a.dim + e : 0), ok);
-            }
+          for (int j = 0; j < VB / 8; ++j) {
+            const uint2 x = load8(v + tk * a.dim + 8 * j, tk < left && g * VB + 8 * j < a.dim);
+            r.v[i][2 * j] = x.x, r.v[i][2 * j + 1] = x.y;
           }
         }
-        if (lane < 2)
-          copy4(ptx::smem_u32(&scales[s][warp]) + 4 * lane, a.scale + ((int64_t)pid * 2 + lane) * a.Hk + h);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int it = 0; it < ST - 1; ++it) issue(it);
+    Group grp[BUFS];
+    load_k(grp[0], 0);
+    load_v(grp[0], 0);
 
     // ---- q: row 8 nt + g of the tile, elements c D / 4 .. of it
     uint32_t q[NT][MT][2];
@@ -234,39 +263,40 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    for (int it = 0; it < nu; ++it) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
-      __syncwarp();                         // the scales came by lanes 0 and 1
-      const int s = it % ST;
-      const bool have = (ready >> s) & 1;
-      issue(it + ST - 1);
-      if (!have) continue;
+    // group it, whose registers then take group it + BUFS
+    auto group = [&](Group& r, int it) {
       const int tok = tok0 + it * kFUnit;
-      const uint4* mine = reinterpret_cast<const uint4*>(smem) + (size_t)s * NP * kFThreads + tid;
+      const bool have = r.at != nullptr;
       float sc[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      if (have) {
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        const uint4 lo = mine[j * kFThreads], hi = mine[(KT + j) * kFThreads];
-        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+        for (int j = 0; j < KT; ++j) {
+          const uint32_t wl[4] = {r.k[j].x, r.k[j].y, r.k[j].z, r.k[j].w};
+          const uint32_t wh[4] = {r.k[KT + j].x, r.k[KT + j].y, r.k[KT + j].z, r.k[KT + j].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t af[4] = {halves(wl[i]), halves(wh[i]), halves_hi(wl[i]), halves_hi(wh[i])};
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t af[4] = {halves(wl[i]), halves(wh[i]), halves_hi(wl[i]), halves_hi(wh[i])};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            ptx::mma_16816<false>(sc[nt], af, q[nt][4 * j + i][0], q[nt][4 * j + i][1]);
+            for (int nt = 0; nt < NT; ++nt)
+              ptx::mma_16816<false>(sc[nt], af, q[nt][4 * j + i][0], q[nt][4 * j + i][1]);
+          }
         }
       }
-      const float2 kv = scales[s][warp];
-      const float lv = log2f(kv.y), inv = 1.f / kv.y;
+      const float ks = r.ks, lv = log2_fast(r.vs), inv = inverse_fast(r.vs);
+      load_k(r, it + BUFS);                 // (r.at is the next group's from here on)
+      if (!have) {
+        load_v(r, it + BUFS);
+        return;
+      }
       const bool edge = tok + 15 > pos_low || (a.window > 0 && tok <= pos_high - a.window);
       uint32_t p[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fmaf(sc[nt][i], kv.x * cs[nt][i & 1], lv);
+        for (int i = 0; i < 4; ++i) x[i] = fmaf(sc[nt][i], ks * cs[nt][i & 1], lv);
         if (edge) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -304,29 +334,10 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         p[nt][1] = transpose8x8(Elem<__half>::pack2(e2, e3));
       }
       // v: words of 4 elements of the 4 tokens -> pairs of tokens of one element
-      uint32_t wv[4][VB / 4];
-      if constexpr (VB % 16 == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < VB / 16; ++j) {
-            const uint4 v = mine[(KP + i * (VB / 16) + j) * kFThreads];
-            wv[i][4 * j] = v.x, wv[i][4 * j + 1] = v.y, wv[i][4 * j + 2] = v.z, wv[i][4 * j + 3] = v.w;
-          }
-      } else {
-        const uint2* m2 = reinterpret_cast<const uint2*>(reinterpret_cast<const uint4*>(smem) + (size_t)(s * NP + KP) * kFThreads) + tid;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < VB / 8; ++j) {
-            const uint2 v = m2[(i * (VB / 8) + j) * kFThreads];
-            wv[i][2 * j] = v.x, wv[i][2 * j + 1] = v.y;
-          }
-      }
 #pragma unroll
       for (int j = 0; j < VB / 4; ++j) {
-        const uint32_t x0 = __byte_perm(wv[0][j], wv[1][j], 0x5140), x1 = __byte_perm(wv[0][j], wv[1][j], 0x7362);
-        const uint32_t y0 = __byte_perm(wv[2][j], wv[3][j], 0x5140), y1 = __byte_perm(wv[2][j], wv[3][j], 0x7362);
+        const uint32_t x0 = __byte_perm(r.v[0][j], r.v[1][j], 0x5140), x1 = __byte_perm(r.v[0][j], r.v[1][j], 0x7362);
+        const uint32_t y0 = __byte_perm(r.v[2][j], r.v[3][j], 0x5140), y1 = __byte_perm(r.v[2][j], r.v[3][j], 0x7362);
         const uint32_t a0[4] = {halves(x0), halves_hi(x0), halves(y0), halves_hi(y0)};
         const uint32_t a1[4] = {halves(x1), halves_hi(x1), halves(y1), halves_hi(y1)};
 #pragma unroll
@@ -335,10 +346,20 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
           ptx::mma_16816<false>(o[nt][2 * j + 1], a1, p[nt][0], p[nt][1]);
         }
       }
+      load_v(r, it + BUFS);
+    };
+    if constexpr (BUFS == 2) {
+      load_k(grp[1], 1);
+      load_v(grp[1], 1);
+      for (int it = 0; it < nu; it += 2) {
+        group(grp[0], it);
+        group(grp[1], it + 1);
+      }
+    } else {
+      for (int it = 0; it < nu; ++it) group(grp[0], it);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-    // ---- the warps' sums meet in shared memory, in the stages' place.  Element
+    // ---- the warps' sums meet in shared memory.  Element
     // g VB + 2 mt + e of a row lies at mt 16 + 2 g + e: neighbouring lanes write
     // neighbouring words.
     constexpr int LD = D + 8;
@@ -363,8 +384,8 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
       }
     }
     __syncthreads();
-    const bool whole = w == item0 && w + nu == item1;
-    const int which = w == item0 ? 1 : 0;   // an item begun here and not ended is this CTA's last
+    const bool whole = begins && w == item1;
+    const int which = begins ? 1 : 0;       // an item begun here and not ended is this CTA's last
     float* part = part_of<D, NT>(a, blockIdx.x, which);
     for (int i = tid; i < t.rows * (D / 2); i += kFThreads) {
       const int row = i / (D / 2), pr = i % (D / 2), gg = pr / MT, mt = pr % MT, d = gg * VB + 2 * mt;
@@ -419,17 +440,13 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
     }
-    __syncthreads();                        // the stages are free again
-    w += nu;
-    off += nu;
+    __syncthreads();                        // shared memory is free again
   }
 }
 
 template <int D, int NT, typename E>
 cudaError_t few_launch(const AttnArgs& a, cudaStream_t st) {
-  constexpr int stage = FewShape<D>::kStages * (D / 16) * kFThreads * 16;
-  constexpr int acc = kFWarps * 8 * NT * (D + 8) * 4;
-  constexpr int smem = stage > acc ? stage : acc;
+  constexpr int smem = kFWarps * 8 * NT * (D + 8) * 4;
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -439,9 +456,8 @@ cudaError_t few_launch(const AttnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  constexpr int per_sm = D <= 128 ? (NT == 1 ? 4 : 3) : 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(148 * per_sm, 1, 1);
+  cfg.gridDim = dim3(148 * FewShape<D, NT>::kCtas, 1, 1);
   cfg.blockDim = dim3(kFThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

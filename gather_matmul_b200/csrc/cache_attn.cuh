@@ -4,9 +4,10 @@
 //
 // A row is one query of one head.  The rows of a sequence that share a k/v head
 // (its queries times `group` heads, queries outer) are cut into tiles of R rows;
-// an item is (row tile, k/v head); a unit is U of the item's visible tokens.  All
-// units, item after item, are divided evenly among the CTAs, so a batch of ragged
-// lengths and a single long sequence fill the GPU alike.  Every CTA finds its own
+// an item is (row tile, k/v head); a unit is U of the item's visible tokens, or one of
+// `C` idle ones that stand for what an item costs beside its tokens.  All units, item
+// after item, are divided evenly among the CTAs, so a batch of ragged lengths and a
+// single long sequence fill the GPU alike.  Every CTA finds its own
 // share from the lengths.  A CTA whose share ends inside an item leaves the sums
 // of its part in the workspace; the last of an item's CTAs to come adds the parts
 // in order, so results do not depend on which one that is.
@@ -22,24 +23,31 @@ namespace attn {
 // A row tile of a sequence: rows r0 .. r0 + rows of the sequence's n * group,
 // queries in rows q0 .. q0 + n of q, tokens [lo, hi) visible to at least one row.
 struct Tile {
-  int b, q0, n, len, r0, rows, lo, hi, u0, units;
+  int b, q0, n, len, r0, rows, lo, hi, u0, units;   // units: with the idle ones, which come first
 };
 
+// Slots of row tiles: the one of a sequence of few rows is the sequence's number, the
+// tiles of longer ones begin at this.
+template <int R>
+__host__ __device__ __forceinline__ constexpr bool one_tile() { return R <= kFewRows; }
 template <int R>
 __device__ __forceinline__ int64_t slot_of(const AttnArgs& a, int b) {
+  if constexpr (one_tile<R>()) return b;
   if (a.starts == nullptr) return (int64_t)b * ((a.group + R - 1) / R);
   return ((int64_t)a.starts[b] * a.group) / R + b;
 }
 template <int R>
-__host__ __device__ __forceinline__ int64_t slots_of(const AttnArgs& a) {
+__device__ __forceinline__ int64_t slots_of(const AttnArgs& a) {
+  if constexpr (one_tile<R>()) return a.B;
   if (a.starts == nullptr) return (int64_t)a.B * ((a.group + R - 1) / R);
   return ((int64_t)a.T * a.group) / R + a.B;
 }
 // the sequence whose slots hold this one
 template <int R>
 __device__ __forceinline__ int seq_of(const AttnArgs& a, int64_t slot) {
-  int lo = 0, hi = a.B;
+  if constexpr (one_tile<R>()) return (int)slot;
   if (a.starts == nullptr) return (int)min(slot / ((a.group + R - 1) / R), (int64_t)a.B - 1);
+  int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (slot_of<R>(a, mid) <= slot) lo = mid;
@@ -49,7 +57,7 @@ __device__ __forceinline__ int seq_of(const AttnArgs& a, int64_t slot) {
 }
 
 // units == 0: the slot holds no rows
-template <int R, int U>
+template <int R, int U, int C>
 __device__ __forceinline__ void tile_of(const AttnArgs& a, int b, int64_t slot, Tile& t) {
   t.b = b;
   t.q0 = b;
@@ -69,7 +77,7 @@ __device__ __forceinline__ void tile_of(const AttnArgs& a, int b, int64_t slot, 
   t.hi = max(p1 + 1, 0);
   t.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), t.hi) : 0;
   t.u0 = t.lo / U;
-  t.units = max((t.hi + U - 1) / U - t.u0, 1);   // one even where nothing is visible: its rows are zero
+  t.units = C + max((t.hi + U - 1) / U - t.u0, 1);   // one even where nothing is visible: its rows are zero
 }
 
 struct Shared {
@@ -82,7 +90,7 @@ struct Shared {
 // This CTA's share [w0, w1) of all units, and the first one's slot, sequence and
 // place among the slot's units (of all k/v heads).  Every thread calls it.  CTAs
 // past `ctas` get nothing.
-template <int R, int U>
+template <int R, int U, int C>
 __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_units, unsigned long long& w0,
                                        unsigned long long& w1, unsigned long long& all, int& ctas) {
   const int64_t slots = slots_of<R>(a);
@@ -94,7 +102,7 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
   Tile t;
   for (int64_t s = s0; s < s1; ++s) {
     while (b + 1 < a.B && slot_of<R>(a, b + 1) <= s) ++b;
-    tile_of<R, U>(a, b, s, t);
+    tile_of<R, U, C>(a, b, s, t);
     mine += (unsigned long long)t.units * a.Hk;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -125,7 +133,7 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
     b = first;
     for (int64_t s = s0; s < s1; ++s) {
       while (b + 1 < a.B && slot_of<R>(a, b + 1) <= s) ++b;
-      tile_of<R, U>(a, b, s, t);
+      tile_of<R, U, C>(a, b, s, t);
       const unsigned long long u = (unsigned long long)t.units * a.Hk;
       if (w0 < at + u) {
         sm.slot = (int)s;

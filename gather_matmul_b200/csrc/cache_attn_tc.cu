@@ -101,7 +101,7 @@ struct Cursor {
     if (w >= w1) return false;
     for (;;) {
       while (seq + 1 < a.B && slot_of<R>(a, seq + 1) <= slot) ++seq;
-      tile_of<R, kN>(a, seq, slot, t);
+      tile_of<R, kN, 0>(a, seq, slot, t);
       const unsigned long long slot_units = (unsigned long long)t.units * a.Hk;
       if (off < slot_units) break;
       off -= slot_units;
@@ -231,7 +231,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
   ptx::tc_fence_before();
   unsigned long long w0, w1, all;
   int ctas;
-  divide<M::kRows, kN>(a, sm.div, 2, w0, w1, all, ctas);   // __syncthreads
+  divide<M::kRows, kN, 0>(a, sm.div, 2, w0, w1, all, ctas);   // __syncthreads
   ptx::tc_fence_after();
   const uint32_t tmem = same(sm.tmem);
   const int steps = same((int)(w1 - w0));
