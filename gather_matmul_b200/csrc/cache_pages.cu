@@ -181,6 +181,7 @@ pages_free_kernel(const __grid_constant__ PagePlanArgs a, const int32_t* seqs) {
 // ---------------------------------------------------------------- fork
 __global__ void __launch_bounds__(kPThreads) pages_fork_kernel(const __grid_constant__ PagePlanArgs a) {
   __shared__ PlanShared sm;
+  __shared__ int3 rows[kPThreads];              // source, target, full pages of this CTA's pairs
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
   cg::cluster_group cl = cg::this_cluster();
@@ -229,7 +230,8 @@ __global__ void __launch_bounds__(kPThreads) pages_fork_kernel(const __grid_cons
     }
   }
   if (i == 0) *a.count = min(total.x, total.y);
-  cl.sync();                                    // every claim has been read
+  rows[threadIdx.x] = make_int3(s, d, ok ? full : 0);
+  cl.sync();                                    // every claim has been read, every row is known
   if (d >= 0 && d < a.B && i < a.n) {
     if (ok) {
       a.lengths[d] = len;
@@ -238,19 +240,20 @@ __global__ void __launch_bounds__(kPThreads) pages_fork_kernel(const __grid_cons
       a.lengths[d] = 0;
     }
   }
-  for (unsigned todo = __ballot_sync(~0u, ok && full > 0); todo; todo &= todo - 1) {
-    const int l = __ffs(todo) - 1;
-    const int ls = __shfl_sync(~0u, s, l), ld = __shfl_sync(~0u, d, l), lf = __shfl_sync(~0u, full, l);
-    for (int j = lane; j < lf; j += 32) {
-      const int p = a.tables[(int64_t)ls * a.M + j];
+  // the shared pages: pair after pair over all warps of the cluster
+  for (int k = i >> 5; k < a.n; k += kPAll / 32) {
+    const int3 r = cl.map_shared_rank(rows, k / kPThreads)[k % kPThreads];
+    for (int j = lane; j < r.z; j += 32) {
+      const int p = a.tables[(int64_t)r.x * a.M + j];
       if (p < 0 || p >= a.P) {
         atomicAdd(a.bad, 1);
         continue;
       }
-      a.tables[(int64_t)ld * a.M + j] = p;
+      a.tables[(int64_t)r.y * a.M + j] = p;
       atomicAdd(a.refs + p, 1);
     }
   }
+  cl.sync();                                    // nobody leaves while its rows are read
 }
 
 // ---------------------------------------------------------------- compact

@@ -7,8 +7,8 @@
 // begun already keeps its scale or, when a new token needs a larger one, its
 // values are divided by the quotient of the two and rounded once more.
 //
-// One warp holds 16 tokens of one head of k or v in registers (read once),
-// page / 16 warps meet in shared memory for the maximum.  Bound by memory: two
+// Several tokens: one warp holds 16 tokens of one head of k or v in registers (read
+// once), page / 16 warps meet in shared memory for the maximum.  Bound by memory: two
 // bytes read and one written for each element.
 #include "cache.h"
 #include "common.cuh"
@@ -53,7 +53,7 @@ __device__ __forceinline__ float power_scale(float a) {
 
 // NC: 16-byte pieces (8 elements) that a lane holds of its warp's 16 tokens, at most
 template <typename E, int NC>
-__global__ void __launch_bounds__(kWThreads)
+__global__ void __launch_bounds__(kWThreads, NC <= 8 ? 4 : 2)
 cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
   __shared__ uint32_t warp_max[kWThreads / 32];
   ptx::grid_dep_wait();
@@ -68,35 +68,26 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
 
   // the slot's sequence and page: sequence b owns the slots from starts[b] / page + 2 b,
   // as many as its new tokens can touch pages
-  int b, row0 = 0, n = 1, touch = 0;
-  bool live = true;
-  if (a.starts == nullptr) {
-    b = (int)slot;
-    live = slot < a.B;
-    row0 = b;
-  } else {
-    int lo = 0, hi = a.B;                                  // first slot of lo <= slot < that of hi
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int at = lo + lane * step;
-      const bool below = at < hi && (int64_t)(a.starts[at] >> a.page_log) + 2 * at <= slot;
-      const int k = max(31 - __clz(__ballot_sync(~0u, below)), 0);
-      lo += k * step;
-      hi = min(hi, lo + step);
-    }
-    b = lo;
-    const int s0 = a.starts[b], s1 = a.starts[b + 1];
-    row0 = min(max(s0, 0), a.T);
-    n = min(max(s1, row0), a.T) - row0;
-    if ((s0 < 0 || s1 < s0 || s1 > a.T) && side == 0 && sub == 0 && lane == 0) atomicAdd(a.bad + 1, 1);
-    const int64_t t = slot - (s0 >> a.page_log) - 2 * (int64_t)b;
-    live = t >= 0 && t < 0x7fffffff;
-    touch = live ? (int)t : 0;
+  int lo = 0, hi = a.B;                                     // first slot of lo <= slot < that of hi
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < hi && (int64_t)(a.starts[at] >> a.page_log) + 2 * at <= slot;
+    const int k = max(31 - __clz(__ballot_sync(~0u, below)), 0);
+    lo += k * step;
+    hi = min(hi, lo + step);
   }
+  const int b = lo;
+  const int s0 = a.starts[b], s1 = a.starts[b + 1], len = a.lengths[b];
+  int row0 = min(max(s0, 0), a.T);
+  const int n = min(max(s1, row0), a.T) - row0;
+  if ((s0 < 0 || s1 < s0 || s1 > a.T) && side == 0 && sub == 0 && lane == 0) atomicAdd(a.bad + 1, 1);
+  const int64_t t = slot - (s0 >> a.page_log) - 2 * (int64_t)b;
+  bool live = t >= 0 && t < 0x7fffffff;
+  const int touch = live ? (int)t : 0;
   int first = 0, last = 0, page_at = 0, begun = 0;          // new positions [first, last) of this page
   int64_t pid = -1;
   if (live) {
-    const int len = a.lengths[b];
     const int p0 = max(len - n, 0);
     const int64_t pi = (int64_t)(p0 >> a.page_log) + touch;
     live = len > 0 && n > 0 && (pi << a.page_log) < len;
@@ -107,10 +98,6 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
       begun = first - page_at;
       row0 += first - (len - n);
       pid = pi < a.M ? a.tables[(int64_t)b * a.M + pi] : -1;
-      if (pid < 0 || pid >= a.P) {
-        if (side == 0 && sub == 0 && lane == 0) atomicAdd(a.bad, 1);
-        live = false;
-      }
     }
   }
   const bool is_v = side >= a.Hk;
@@ -131,6 +118,13 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
         r[k] = ldg_stream(x + (int64_t)(row0 + t - first) * ld + 8 * (i - row * per_row));
     }
   }
+  if (live && (pid < 0 || pid >= a.P)) {                    // looked at once x is on its way
+    if (side == 0 && sub == 0 && lane == 0) atomicAdd(a.bad, 1);
+    live = false;
+  }
+  const int64_t place = pid * sides + side;
+  float before = 0.f;
+  if (live && begun) before = a.scale[place];
   // 16-bit magnitudes order as their bits do; infinities and NaN come out on top
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
@@ -146,14 +140,9 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
     for (int i = 0; i < wpu; ++i) top = max(top, warp_max[(warp & ~(wpu - 1)) + i]);
   }
   if (!live) return;
-  const int64_t place = pid * sides + side;
   float s = power_scale(Elem<E>::to_f32((uint16_t)top));
-  float before = s;
-  if (begun) {
-    before = a.scale[place];
-    // a page whose scale is NaN stays so
-    s = before >= s ? before : (before < s ? s : before + s);
-  }
+  if (begun) s = before >= s ? before : (before < s ? s : before + s);   // NaN stays NaN
+  else before = s;
   if (wpu > 1) {
     // every warp has read the old scale; the barrier counts the unit's own warps only
     asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpu), "r"(wpu * 32) : "memory");
@@ -190,11 +179,66 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
   }
 }
 
-template <typename E, int NC>
-cudaError_t write_launch(const CacheWriteArgs& a, cudaStream_t st) {
-  const int64_t slots = a.starts ? (int64_t)(a.T >> a.page_log) + 2 * (int64_t)a.B : a.B;
-  const int64_t warps = (slots * 2 * a.Hk) << (a.page_log - 4);
-  const int64_t ctas = (warps + kWThreads / 32 - 1) / (kWThreads / 32);
+// Single tokens: LANES lanes, of 8 elements each, for a head of k or v; little to hold
+// for each, so that all of a decode batch is on the GPU at once.
+template <typename E, int LANES>
+__global__ void __launch_bounds__(kWThreads)
+cache_write_single_kernel(const __grid_constant__ CacheWriteArgs a) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch_dependents();
+  const int sides = 2 * a.Hk, lane = threadIdx.x & (LANES - 1);
+  const int64_t unit = ((int64_t)blockIdx.x * kWThreads + threadIdx.x) / LANES;
+  const int64_t seq = unit / sides;
+  const int side = (int)(unit - seq * sides), b = (int)min(seq, (int64_t)a.B - 1);
+  const int len = a.lengths[b];
+  bool live = seq < a.B && len > 0;
+  const int at = max(len - 1, 0), page = 1 << a.page_log, begun = at & (page - 1);
+  int64_t pid = -1;
+  if (live && at >> a.page_log < a.M) pid = a.tables[(int64_t)b * a.M + (at >> a.page_log)];
+  const bool is_v = side >= a.Hk;
+  const E* x = static_cast<const E*>(is_v ? a.v : a.k) + (int64_t)b * (is_v ? a.ldv : a.ldk) +
+               (int64_t)(is_v ? side - a.Hk : side) * a.dim;
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (live && 8 * lane < a.dim) r = ldg_stream(x + 8 * lane);
+  if (live && (pid < 0 || pid >= a.P)) {
+    if (side == 0 && lane == 0) atomicAdd(a.bad, 1);
+    live = false;
+  }
+  const int64_t place = pid * sides + side;
+  float before = 0.f;
+  if (live && begun) before = a.scale[place];
+  const uint32_t m = __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu), __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu));
+  uint32_t top = max(m & 0xffffu, m >> 16);
+#pragma unroll
+  for (int d = 1; d < LANES; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
+  if (!live) return;
+  float s = power_scale(Elem<E>::to_f32((uint16_t)top));
+  if (begun) s = before >= s ? before : (before < s ? s : before + s);   // NaN stays NaN
+  else before = s;
+  uint8_t* out = a.cache + (place << a.page_log) * a.dim;
+  if (before != s && before == before && s == s) {
+    const float ratio = before / s;
+    for (int i = lane; i < begun * (a.dim >> 4); i += LANES) {
+      uint4* p = reinterpret_cast<uint4*>(out) + i;
+      uint4 v = *p;
+      v = make_uint4(rescale4(v.x, ratio), rescale4(v.y, ratio), rescale4(v.z, ratio), rescale4(v.w, ratio));
+      *p = v;
+    }
+  }
+  if (lane == 0) a.scale[place] = s;
+  if (8 * lane < a.dim) {
+    const float inv = 1.f / s;                              // exact: a power of two
+    float f[8];
+    Elem<E>::to_f32(r, f);
+    uint2 w;
+    w.x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
+    w.y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
+    *reinterpret_cast<uint2*>(out + (int64_t)begun * a.dim + 8 * lane) = w;
+  }
+}
+
+template <typename K>
+cudaError_t launch_ctas(K kernel, const CacheWriteArgs& a, int64_t ctas, cudaStream_t st) {
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, 1, 1);
@@ -203,11 +247,28 @@ cudaError_t write_launch(const CacheWriteArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return counted_launch(cudaLaunchKernelEx(&cfg, cache_write_kernel<E, NC>, a));
+  return counted_launch(cudaLaunchKernelEx(&cfg, kernel, a));
+}
+
+template <typename E, int LANES>
+cudaError_t single_launch(const CacheWriteArgs& a, cudaStream_t st) {
+  return launch_ctas(cache_write_single_kernel<E, LANES>, a, ((int64_t)a.B * 2 * a.Hk * LANES + kWThreads - 1) / kWThreads, st);
+}
+
+template <typename E, int NC>
+cudaError_t write_launch(const CacheWriteArgs& a, cudaStream_t st) {
+  const int64_t slots = (int64_t)(a.T >> a.page_log) + 2 * (int64_t)a.B;
+  const int64_t warps = (slots * 2 * a.Hk) << (a.page_log - 4);
+  return launch_ctas(cache_write_kernel<E, NC>, a, (warps + kWThreads / 32 - 1) / (kWThreads / 32), st);
 }
 
 template <typename E>
 cudaError_t write_width(const CacheWriteArgs& a, cudaStream_t st) {
+  if (a.starts == nullptr) {
+    if (a.dim <= 64) return single_launch<E, 8>(a, st);
+    if (a.dim <= 128) return single_launch<E, 16>(a, st);
+    return single_launch<E, 32>(a, st);
+  }
   if (a.dim <= 64) return write_launch<E, 4>(a, st);
   if (a.dim <= 128) return write_launch<E, 8>(a, st);
   return write_launch<E, 16>(a, st);

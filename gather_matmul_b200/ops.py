@@ -508,36 +508,40 @@ def norm_rope(x: torch.Tensor, weights, y: torch.Tensor, heads: Sequence[int], h
 # device.
 # ---------------------------------------------------------------------------
 def _ints(t, name, shape):
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.shape != shape:
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
 
 
 def _list(t, name):
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.dim() != 1:
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor of one dimension")
-    return _int(name, t.numel())
+    return _int(name, t.shape[0])
 
 
 def _cache(cache, scale, layers):
-    """(layers, pages, kv_heads, page_tokens, head_dim); layers 0: of one layer, without that dimension."""
-    if cache.dtype is not _FP8 or not cache.is_contiguous() or cache.dim() != 5 + layers or \
-            cache.shape[1 + layers] != 2:
+    """The cache's dimensions: [layers,] pages, 2, kv_heads, page_tokens, head_dim."""
+    shape = cache.shape
+    if cache.dtype is not _FP8 or len(shape) != 5 + layers or shape[1 + layers] != 2 or \
+            not cache.is_contiguous():
         raise TypeError("cache must be a contiguous float8_e4m3fn tensor of " +
                         ("layers x " if layers else "") + "pages x 2 x kv_heads x page_tokens x head_dim")
-    if scale.dtype is not torch.float32 or not scale.is_contiguous() or \
-            scale.shape != cache.shape[:3 + layers]:
+    if scale.dtype is not torch.float32 or scale.shape != shape[:3 + layers] or not scale.is_contiguous():
         raise TypeError("scale must be a contiguous float32 tensor of the cache's first dimensions")
-    shape = tuple(_int("cache", v) for v in cache.shape)
-    return (shape[0] if layers else 1, shape[layers], *shape[2 + layers:])
+    if max(shape) > _INT_MAX:
+        raise LoraError("lora_cache", _lib.LORA_ERR_UNSUPPORTED)
+    return shape
 
 
 def _seqs(tables, lengths=None):
-    if tables.dtype is not torch.int32 or not tables.is_contiguous() or tables.dim() != 2:
+    shape = tables.shape
+    if tables.dtype is not torch.int32 or len(shape) != 2 or not tables.is_contiguous():
         raise TypeError("tables must be a contiguous int32 tensor of sequences x pages")
-    B, M = tables.shape
-    if lengths is not None:
-        _ints(lengths, "lengths", (B,))
-    return _int("tables", B), _int("tables", M)
+    if max(shape) > _INT_MAX:
+        raise LoraError("lora_cache", _lib.LORA_ERR_UNSUPPORTED)
+    if lengths is not None and (lengths.dtype is not torch.int32 or lengths.shape != shape[:1] or
+                                not lengths.is_contiguous()):
+        raise TypeError("lengths must be a contiguous int32 tensor of one length per sequence")
+    return shape
 
 
 def _work(work):
@@ -575,7 +579,7 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, scale: to
     lengths: tokens of each sequence, the new ones counted in; starts: int32
     [B + 1], the new tokens of sequence b are rows starts[b] .. starts[b+1]
     (None: one row each); the pages must be there (pages_extend)."""
-    _, P, H, page, dim = _cache(cache, scale, 0)
+    P, _, H, page, dim = _cache(cache, scale, 0)
     B, M = _seqs(tables, lengths)
     T = k.shape[0]
     ldk = _new_rows(k, "k", H * dim, starts, B)
@@ -600,7 +604,7 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor, t
     if window > 0).  q, y: fp16/bf16 [T, q_heads * head_dim]; lengths, starts as
     for cache_write, which comes first; softmax_scale: 1 / sqrt(head_dim) by
     default.  Queries that see nothing get zeros."""
-    _, P, H, page, dim = _cache(cache, scale, 0)
+    P, _, H, page, dim = _cache(cache, scale, 0)
     B, M = _seqs(tables, lengths)
     T, width = q.shape[0], q.shape[1] if q.dim() == 2 else -1
     if width <= 0 or width % (H * dim):
@@ -653,7 +657,7 @@ def pages_fork(tables: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, 
     """Each empty row dst[i] becomes a copy of the sequence src[i] (int32 [n]):
     full pages are shared, the begun last one is copied in all layers."""
     B, M = _seqs(tables, lengths)
-    L, P, H, page, dim = _cache(cache, scale, 1)
+    L, P, _, H, page, dim = _cache(cache, scale, 1)
     _ints(refs, "refs", (P,))
     n = _list(src, "src")
     _ints(dst, "dst", (n,))
@@ -672,7 +676,7 @@ def pages_compact(tables: torch.Tensor, refs: torch.Tensor, cache: torch.Tensor,
     and counts follow, in place or into out_tables and out_refs.  n_live: int32
     [1], receives the number of live pages."""
     B, M = _seqs(tables)
-    L, P, H, page, dim = _cache(cache, scale, 1)
+    L, P, _, H, page, dim = _cache(cache, scale, 1)
     _ints(refs, "refs", (P,))
     out_tables = tables if out_tables is None else out_tables
     out_refs = refs if out_refs is None else out_refs
@@ -693,7 +697,7 @@ def pages_copy(cache: torch.Tensor, scale: torch.Tensor, src: torch.Tensor, dst:
                work: torch.Tensor, stream=None):
     """Copy page src[i] to page dst[i] (int32 [n]) in all layers, with its
     scales.  No page may be the target of two pairs, or target and source."""
-    L, P, H, page, dim = _cache(cache, scale, 1)
+    L, P, _, H, page, dim = _cache(cache, scale, 1)
     n = _list(src, "src")
     _ints(dst, "dst", (n,))
     wp, wn = _work(work)
