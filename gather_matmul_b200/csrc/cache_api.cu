@@ -37,7 +37,7 @@ lora_status check_cache(int pages, int kv_heads, int page_tokens, int dim) {
 // tables of n sequences of up to m pages
 lora_status check_seqs(int n, int m) {
   if (n < 0 || m <= 0) return LORA_ERR_INVALID_ARG;
-  if (n > LORA_MAX_SEQS || (int64_t)m * 128 > INT_MAX) return LORA_ERR_UNSUPPORTED;
+  if (n > LORA_MAX_SEQS || (int64_t)m * 128 > INT_MAX / 2) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 
@@ -61,7 +61,6 @@ lora_status check_rows(const void* p, int64_t ld, int64_t width) {
   return LORA_OK;
 }
 
-// room > 0: the plan arrays of `room` pages are needed too
 lora_status check_work(const void* work, size_t bytes, size_t need) {
   if (work == nullptr || bytes < need) return LORA_ERR_INVALID_ARG;
   return aligned(work, 256) ? LORA_OK : LORA_ERR_MISALIGNED;
@@ -121,7 +120,7 @@ lora_status lora_cache_write(lora_dtype dtype, int T, int n_seqs, int kv_heads, 
   a.page_log = log2_of(page_tokens);
   a.P = n_pages;
   a.M = max_pages;
-  // one CTA at least for eight warps of 16 tokens of a head: the grid's limit
+  // eight warps of 16 tokens of a head in a CTA: the grid's limit
   const int64_t slots = starts ? (int64_t)(T >> a.page_log) + 2 * (int64_t)n_seqs : n_seqs;
   if (((slots * 2 * kv_heads) << (a.page_log - 4)) / 8 >= INT_MAX) return LORA_ERR_UNSUPPORTED;
   cudaGetLastError();

@@ -105,6 +105,7 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
   const int64_t ld = is_v ? a.ldv : a.ldk;
   x += (int64_t)(is_v ? side - a.Hk : side) * a.dim;
   const int per_row = a.dim >> 3, nc = a.dim >> 4;          // pieces of a token, and of a lane
+  const int inv_row = (65535 + per_row) / per_row;          // i / per_row, exact for i < 512
   const int t0 = page_at + sub * 16;
 
   uint4 r[NC];
@@ -113,7 +114,7 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
   for (int k = 0; k < NC; ++k) {
     r[k] = make_uint4(0, 0, 0, 0);
     if (k < nc && live) {
-      const int i = lane + 32 * k, row = i / per_row, t = t0 + row;
+      const int i = lane + 32 * k, row = i * inv_row >> 16, t = t0 + row;
       if (t >= first && t < last)
         r[k] = ldg_stream(x + (int64_t)(row0 + t - first) * ld + 8 * (i - row * per_row));
     }
@@ -166,7 +167,7 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     if (k < nc) {
-      const int i = lane + 32 * k, row = i / per_row, t = t0 + row;
+      const int i = lane + 32 * k, row = i * inv_row >> 16, t = t0 + row;
       if (t >= first && t < last) {
         float f[8];
         Elem<E>::to_f32(r[k], f);

@@ -1,9 +1,14 @@
-"""The attention inputs of one decoder layer whose q/k/v projection carries
-LoRA adapters: the library's calls in the order a serving step makes them.
+"""The attention of one decoder layer whose q/k/v projection carries LoRA
+adapters: the library's calls in the order a serving step makes them.
 
+AttentionInputs
   y        = x W^T                                   linear_fp8
   y       += scale (x A[idx]^T) B[idx]^T  per slice  bgmv
   y[q, k]  = rotation of (the norms of) the heads    norm_rope / rope, in place
+
+CachedAttention
+  cache   <- y[k], y[v] in 8 bits                    cache_write
+  out      = softmax(c y[q] k^T) v over the cache    cache_attention
 
 All work is enqueued on the current stream; no call allocates, so a step can
 be captured in a CUDA graph.
@@ -84,3 +89,46 @@ class AttentionInputs:
         return ops.norm_rope(y, self.norms, y, self.heads, self.head_dim, positions, self.inv_freq,
                              eps=self.eps, interleaved=self.interleaved,
                              attn_scale=self.attn_scale)
+
+
+class CachedAttention:
+    """A layer's attention over its part of a paged 8-bit cache, behind its
+    AttentionInputs.
+
+    cache, scale   this layer's float8_e4m3fn [pages, 2, kv_heads, page_tokens,
+                   head_dim] and float32 [pages, 2, kv_heads], as for
+                   ops.cache_write.
+    work           ops.cache_workspace of that many pages; the layers of a model,
+                   which run one after another, can share one (None: its own).
+    softmax_scale, window   as for ops.cache_attention.
+
+    The sequences' pages must be there (ops.pages_extend), for all layers at once.
+    """
+
+    def __init__(self, inputs: AttentionInputs, cache: torch.Tensor, scale: torch.Tensor,
+                 work: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+                 window: int = 0):
+        kv_heads, dim = inputs.heads[1], inputs.head_dim
+        if cache.dim() != 5 or cache.shape[2] != kv_heads or cache.shape[4] != dim:
+            raise ValueError(f"cache must hold {kv_heads} heads of {dim}")
+        if cache.device != inputs.W.device or scale.device != inputs.W.device:
+            raise ValueError("cache and scale must be on W's device")
+        self.inputs, self.cache, self.scale = inputs, cache, scale
+        self.work = ops.cache_workspace(cache.shape[0], dim, cache.device) if work is None else work
+        self.softmax_scale, self.window = softmax_scale, window
+
+    def __call__(self, x: torch.Tensor, idx: torch.Tensor, positions: torch.Tensor,
+                 tables: torch.Tensor, lengths: torch.Tensor, y: torch.Tensor, out: torch.Tensor,
+                 starts: Optional[torch.Tensor] = None, has_lora: Optional[bool] = None,
+                 idx_host=None) -> torch.Tensor:
+        """out [T, q_heads * head_dim] of the new tokens x [T, K]; y [T, N] receives
+        q, k and v.  tables, lengths (the new tokens counted in) and starts as
+        for ops.cache_attention, idx, positions, has_lora, idx_host as for
+        AttentionInputs."""
+        self.inputs(x, idx, positions, y, has_lora=has_lora, idx_host=idx_host)
+        (hq, hk), dim = self.inputs.heads, self.inputs.head_dim
+        k, v = hq * dim, (hq + hk) * dim
+        ops.cache_write(y[:, k:v], y[:, v:v + hk * dim], self.cache, self.scale, tables, lengths,
+                        self.work, starts)
+        return ops.cache_attention(y[:, :k], self.cache, self.scale, tables, lengths, out, self.work,
+                                   starts, self.softmax_scale, self.window)
