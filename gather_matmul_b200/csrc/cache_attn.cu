@@ -13,11 +13,15 @@
 // Products run on mma.sync with the tokens (k) and the head's elements (v) on the
 // wide side, M = 16, and the rows on the narrow one, N = 8: a tile of 8 rows costs
 // half of what it would cost as M = 16.  e4m3 becomes fp16 exactly, in registers.
-// The order of the products' inner indices is free, so every thread copies 16-byte
-// pieces of its own (cp.async) and reads back just those: no transposes, no
-// barriers, and what is in flight sits in shared memory.  q's rows are brought to
-// fp16 by powers of two (their largest elements to 2^7 .. 2^8), which costs less
-// than the rounding of the sums.
+// The order of the products' inner indices is free, so every thread loads 16-byte
+// pieces and needs no others: no transposes, no barriers, no shared memory before a
+// warp's sums are done.  The next group of tokens is loaded into the registers that the
+// products have just read.  q's rows are brought to fp16 by powers of two (their largest
+// elements to 2^7 .. 2^8), which costs less than the rounding of the sums.
+//
+// 128 sequences of 4096 tokens, 32 heads on 8 of 128: 198 us, 5.4 TB/s, 0.83 of the
+// measured copy rate; 512 ragged ones of up to 8192: 227 us, 0.75 (through stages in
+// shared memory, by cp.async: 407 before the idle units below, 352 in registers).
 #include <cfloat>
 
 #include "cache_attn.cuh"
@@ -31,14 +35,14 @@ using namespace attn;
 
 constexpr int kFThreads = 128, kFWarps = 4;
 constexpr int kFUnit = 64;                  // tokens of a unit: 16 for each warp
-constexpr int kIdle = 2;                    // what an item costs beside its tokens, in units
+// What an item costs beside its tokens, in units: CTAs of many short sequences get
+// fewer.  The ragged batch above: 0 units 352 us, 1 264, 2 231, 4 250, 8 264.
+constexpr int kIdle = 2;
 constexpr float kShift = 6.f, kSlack = 8.f;
 
-// Groups of 16 tokens that a warp has in registers, and CTAs that share an SM.
-template <int D, int NT> struct FewShape {
-  static constexpr int kBufs = 1;
-  static constexpr int kCtas = D <= 128 ? (NT == 1 ? 4 : 3) : 2;
-};
+// Four CTAs share an SM where their registers do.  A second group in flight for each
+// warp leaves room for three: 367 us against 352 (the ragged batch, in the form of then).
+template <int D, int NT> constexpr int few_ctas() { return D <= 128 ? (NT == 1 ? 4 : 3) : 2; }
 
 // 16 or 8 bytes, or zeros; no branch, so that loads follow one another
 __device__ __forceinline__ uint4 load16(const void* p, bool in) {
@@ -99,9 +103,9 @@ __device__ __forceinline__ void put_row(const AttnArgs& a, const Tile& t, int h,
 }
 
 template <int D, int NT, typename E>
-__global__ void __launch_bounds__(kFThreads, FewShape<D, NT>::kCtas)
+__global__ void __launch_bounds__(kFThreads, few_ctas<D, NT>())
 attention_few_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int R = 8 * NT, BUFS = FewShape<D, NT>::kBufs;
+  constexpr int R = 8 * NT;
   constexpr int KT = D / 64;               // 16-byte pieces of k of a token that a thread holds (of 2 tokens)
   constexpr int MT = D / 16;               // m-tiles of the v product, and words of k of a token
   constexpr int VB = D / 8;                // bytes of v of one token (4 tokens)
@@ -207,9 +211,9 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
     };
-    Group grp[BUFS];
-    load_k(grp[0], 0);
-    load_v(grp[0], 0);
+    Group r;
+    load_k(r, 0);
+    load_v(r, 0);
 
     // ---- q: row 8 nt + g of the tile, elements c D / 4 .. of it
     uint32_t q[NT][MT][2];
@@ -263,8 +267,8 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // group it, whose registers then take group it + BUFS
-    auto group = [&](Group& r, int it) {
+    // group it, whose registers then take the next one
+    auto group = [&](int it) {
       const int tok = tok0 + it * kFUnit;
       const bool have = r.at != nullptr;
       float sc[NT][4];
@@ -285,9 +289,9 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
       const float ks = r.ks, lv = log2_fast(r.vs), inv = inverse_fast(r.vs);
-      load_k(r, it + BUFS);                 // (r.at is the next group's from here on)
+      load_k(r, it + 1);                 // (r.at is the next group's from here on)
       if (!have) {
-        load_v(r, it + BUFS);
+        load_v(r, it + 1);
         return;
       }
       const bool edge = tok + 15 > pos_low || (a.window > 0 && tok <= pos_high - a.window);
@@ -346,18 +350,9 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
           ptx::mma_16816<false>(o[nt][2 * j + 1], a1, p[nt][0], p[nt][1]);
         }
       }
-      load_v(r, it + BUFS);
+      load_v(r, it + 1);
     };
-    if constexpr (BUFS == 2) {
-      load_k(grp[1], 1);
-      load_v(grp[1], 1);
-      for (int it = 0; it < nu; it += 2) {
-        group(grp[0], it);
-        group(grp[1], it + 1);
-      }
-    } else {
-      for (int it = 0; it < nu; ++it) group(grp[0], it);
-    }
+    for (int it = 0; it < nu; ++it) group(it);
 
     // ---- the warps' sums meet in shared memory.  Element
     // g VB + 2 mt + e of a row lies at mt 16 + 2 g + e: neighbouring lanes write
@@ -457,7 +452,7 @@ cudaError_t few_launch(const AttnArgs& a, cudaStream_t st) {
     if (dev < 64) ready[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(148 * FewShape<D, NT>::kCtas, 1, 1);
+  cfg.gridDim = dim3(148 * few_ctas<D, NT>(), 1, 1);
   cfg.blockDim = dim3(kFThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

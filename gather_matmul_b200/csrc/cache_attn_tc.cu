@@ -1,21 +1,29 @@
 // Attention of many queries over the paged 8-bit cache (lora_cache_attention):
-// prompts and chunks of prompts, where the kernel is bound by the products and by
-// the exponentials between them.  The mathematics (weights that carry the v scales,
+// prompts and chunks of prompts.  The mathematics (weights that carry the v scales,
 // a running maximum that is raised late) is that of cache_attn.cu.
 //
 // Products run on tcgen05: S = Q K^T into tensor memory, the weights P back into
 // tensor memory as fp16, O += P V with P from there.  A CTA holds two tiles of 128
-// rows (for heads of up to 128 elements), so that one tile's products run while the
-// other's softmax does, and a step of 128 tokens serves both:
+// rows (one for heads of more than 128 elements), so that k and v are converted once
+// for 256 rows; as fp16 operands q, k and v keep all their bits.  It goes through its
+// items in steps of 128 tokens:
 //
-//   softmax warpgroups (one for each tile, a thread for each row): S from tensor
-//     memory, weights back, the running sums; q into shared memory and the tile's
-//     results out of tensor memory between items
-//   conversion warpgroup: k and v from global memory (two tiles ahead in
-//     registers), e4m3 to fp16, into the swizzled layout that the products read
-//   one thread issues the products
+//   a warpgroup for each tile's softmax, a thread for each row: scores of 64 tokens
+//     from tensor memory, their weights back, the running sums; the products of one
+//     half of a step run while the weights of the other are formed.  Between items it
+//     brings q in and results out, through shared memory, rows side by side
+//   a warpgroup each for k and v: the next tile from global memory in registers, e4m3
+//     to fp16, into the swizzled layouts that the products read
+//   a warp for each tile that issues its products, and one that plans: it looks up
+//     pages and scales of the next steps, four steps at a time, and divides the items
 //
-// e4m3 is converted once for 256 rows; as fp16 operands q, k, v keep all their bits.
+// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1120 us, 920 TFLOP/s,
+// 0.56 of the measured rate of a 16-bit product (a CTA's step 4800 cycles at two tiles).
+// What binds is the data path of shared memory, 128 bytes a cycle, which a step's
+// operands (q and k 1536 cycles, v 512), converted tiles (512), loads (256) and tensor
+// memory traffic (1536) take for 4350.  Measured otherwise: one warpgroup that
+// converts k, then v 1310; scores of 128 tokens at once, which have room for one
+// buffer, 1235; q as an operand from tensor memory, which also leaves room for one, 1370.
 #include <cfloat>
 #include <type_traits>
 
@@ -34,7 +42,8 @@ constexpr float kShift = 6.f, kMost = 32768.f;
 // others is at least 2^kShift / 2^32.
 constexpr float kNothing = 0x1p-60f;
 // Of each 8 pairs of weights, those whose exponentials are formed on the FMA pipe:
-// the special function unit gives 16 a cycle and SM.
+// the special function unit gives 16 a cycle and SM.  None of 8 1230 us, one 1140, two
+// 1120, three 1170 (the case above).
 constexpr uint32_t kPolyPairs = 0x12;
 constexpr int kBlock = 4, kBlocks = 4;        // steps that are planned at once, and such blocks in shared memory
 constexpr int kRing = kBlock * kBlocks;
@@ -54,7 +63,7 @@ template <int D> struct Many {
   static constexpr int kTileBytes = kN * D * 2;         // 128 rows of fp16
   static constexpr int kSmem = kTileBytes * (kTiles + 2 * kBufs) + 1024;
   static constexpr int kPieces = D / 16;                // 16 bytes of e4m3 each, of a conversion thread
-  static constexpr int kCols = 512;                          // tensor memory: S of each tile, O of each tile
+  static constexpr int kCols = 512;                     // tensor memory: scores and O of each tile
 };
 
 // What the other roles need to know of a step, by groups of 16 tokens (which lie
@@ -131,21 +140,22 @@ __device__ __forceinline__ uint32_t halves_hi(uint32_t two) {
   asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(h) : "r"(two));
   return h;
 }
-// {x, y} = {x, y} * s + l, and {x, y} += l
+// {x, y} = {x, y} * s + l
 __device__ __forceinline__ void fma2(float& x, float& y, uint64_t s, uint64_t l) {
   asm("{\n .reg .b64 t;\n mov.b64 t, {%0, %1};\n fma.rn.f32x2 t, t, %2, %3;\n mov.b64 {%0, %1}, t;\n}"
       : "+f"(x), "+f"(y) : "l"(s), "l"(l));
 }
 __device__ __forceinline__ uint64_t twice(float x) { return ptx::pack2(x, x); }
-// 2^x and 2^y on the FMA pipe, for arguments below 2^7: x = n + f with n the nearest
+// 2^x and 2^y on the FMA pipe, arguments past 127 as 127 (a weight that large is seen
+// to be too large whatever it is) and below -126 as -126: x = n + f with n the nearest
 // whole number (it is left in the low bits of x + 1.5 2^23), 2^f by the polynomial of
 // degree 4 whose relative error over |f| <= 1/2 is least (2.6e-6; fitted by
 // reweighted least squares), times 2^n made from bits.  NaN stays NaN.
 __device__ __forceinline__ void exp2_fma(float& x, float& y) {
   constexpr float kMagic = 12582912.f;
   uint64_t v, r, f, p;
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-126.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;\n min.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(-126.f), "f"(127.f));
+  asm("max.NaN.f32 %0, %0, %1;\n min.NaN.f32 %0, %0, %2;" : "+f"(y) : "f"(-126.f), "f"(127.f));
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(twice(kMagic)));
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(r), "l"(twice(-kMagic)));

@@ -237,6 +237,22 @@ def test_sharp_and_flat_softmax(sm, news):
     attend(c, q, torch.full_like(q, math.nan), news, softmax_scale=sm)
 
 
+@pytest.mark.parametrize("jump", [20.0, 60.0, 88.0, 150.0, 1000.0])
+@pytest.mark.parametrize("news", [None, [20] * 40], ids=["single", "chunks"])
+def test_a_score_far_above_all_before_it(jump, news):
+    """One key among zeros, at another place in each sequence: its weight is 2^(1.44 jump) times the others'."""
+    c = Cache([160] * 40, 1, 64, 16, seed=24)
+    c.cache[:, 0] = 0.0
+    c.scale[:, 0] = torch.where(c.scale[:, 0].isnan(), math.nan, 1.0)
+    for b in range(40):
+        at = 60 + 2 * b
+        c.cache[int(c.tables[b, at // 16]), 0, 0, at % 16, 7] = 16.0
+    q = torch.zeros(40 if news is None else sum(news), 2 * 64, device="cuda")
+    q[:, 7] = jump / 16
+    q[:, 64 + 7] = -jump / 16
+    attend(c, q.to(BF16), torch.full(q.shape, math.nan, dtype=BF16, device="cuda"), news, softmax_scale=1.0)
+
+
 @pytest.mark.parametrize("dtype,std", [(F16, 1e-6), (F16, 8000.0), (BF16, 1e-30), (BF16, 1e30)])
 @pytest.mark.parametrize("news", [None, [1, 30, 200]], ids=["single", "chunks"])
 def test_queries_of_all_sizes(dtype, std, news):
