@@ -108,7 +108,8 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int R = 8 * NT;
   constexpr int KT = D / 64;               // 16-byte pieces of k of a token that a thread holds (of 2 tokens)
   constexpr int MT = D / 16;               // m-tiles of the v product, and words of k of a token
-  constexpr int VB = D / 8;                // bytes of v of one token (4 tokens)
+  constexpr int VB = D / 8;                // bytes of v of one token (4 tokens), in pieces of PW
+  constexpr int PW = VB % 16 == 0 ? 16 : 8;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   __shared__ float stat[kFWarps][R][2];
@@ -162,15 +163,16 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
     };
-    // A group in registers: k of tokens g and g + 8, elements from c D / 4 on; v of tokens
-    // 2c, 2c + 1, 2c + 8, 2c + 9, elements from g D / 8 on; the scales.
+    // A group in registers: k of tokens g and g + 8, 16 of each 64 elements from 16 c on; v
+    // of tokens 2c, 2c + 1, 2c + 8, 2c + 9, PW of each 8 PW elements from PW g on (a load's
+    // neighbouring lanes have neighbouring pieces); the scales.
     struct Group {
       uint4 k[2 * KT];
       uint32_t v[4][VB / 4];
       float ks, vs;
       const uint8_t* at;                    // its k in the cache, or null
     };
-    const int k_lane = g * a.dim + c * (D / 4), v_lane = 2 * c * a.dim + g * VB;
+    const int k_lane = g * a.dim + 16 * c, v_lane = 2 * c * a.dim + PW * g;
     auto load_k = [&](Group& r, int it) {
       if ((it & 31) == 0) fetch_pids(it);
       const int pid = __shfl_sync(~0u, pids, it & 31);
@@ -179,9 +181,9 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
       r.at = in ? base + (int64_t)pid * page_bytes + (int64_t)(tok & (page - 1)) * a.dim : nullptr;
 #pragma unroll
       for (int j = 0; j < KT; ++j) {
-        const bool ok = in && c * (D / 4) + 16 * j < a.dim;
-        r.k[j] = load16(r.at + k_lane + 16 * j, ok);
-        r.k[KT + j] = load16(r.at + k_lane + 8 * a.dim + 16 * j, ok);
+        const bool ok = in && 64 * j + 16 * c < a.dim;
+        r.k[j] = load16(r.at + k_lane + 64 * j, ok);
+        r.k[KT + j] = load16(r.at + k_lane + 8 * a.dim + 64 * j, ok);
       }
       r.ks = r.vs = 1.f;
       if (in) {
@@ -199,13 +201,13 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
         if constexpr (VB % 16 == 0) {
 #pragma unroll
           for (int j = 0; j < VB / 16; ++j) {
-            const uint4 x = load16(v + tk * a.dim + 16 * j, tk < left && g * VB + 16 * j < a.dim);
+            const uint4 x = load16(v + tk * a.dim + 128 * j, tk < left && 128 * j + 16 * g < a.dim);
             r.v[i][4 * j] = x.x, r.v[i][4 * j + 1] = x.y, r.v[i][4 * j + 2] = x.z, r.v[i][4 * j + 3] = x.w;
           }
         } else {
 #pragma unroll
           for (int j = 0; j < VB / 8; ++j) {
-            const uint2 x = load8(v + tk * a.dim + 8 * j, tk < left && g * VB + 8 * j < a.dim);
+            const uint2 x = load8(v + tk * a.dim + 64 * j, tk < left && 64 * j + 8 * g < a.dim);
             r.v[i][2 * j] = x.x, r.v[i][2 * j + 1] = x.y;
           }
         }
@@ -215,7 +217,7 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
     load_k(r, 0);
     load_v(r, 0);
 
-    // ---- q: row 8 nt + g of the tile, elements c D / 4 .. of it
+    // ---- q: row 8 nt + g of the tile, the elements that this thread has of k
     uint32_t q[NT][MT][2];
     float cs[NT][2];                        // c * the power of two, of rows 2c and 2c + 1
     int pos[NT][2];                         // their positions; -1: no such row
@@ -224,13 +226,14 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
       const int row = 8 * nt + g, r = t.r0 + row, i = r / a.group;
       const bool in = row < t.rows;
       const E* src = static_cast<const E*>(a.q) + (int64_t)(t.q0 + (in ? i : 0)) * a.ldq +
-                     ((int64_t)h * a.group + (in ? r - i * a.group : 0)) * a.dim + c * (D / 4);
+                     ((int64_t)h * a.group + (in ? r - i * a.group : 0)) * a.dim + 16 * c;
       uint4 v[2 * KT];
       float top = 0.f;
 #pragma unroll
       for (int j = 0; j < 2 * KT; ++j) {
         v[j] = make_uint4(0, 0, 0, 0);
-        if (in && c * (D / 4) + 8 * j < a.dim) v[j] = ldg_nc(src + 8 * j);
+        const int e = 64 * (j / 2) + 8 * (j & 1);
+        if (in && 16 * c + e < a.dim) v[j] = ldg_nc(src + e);
         float f[8];
         Elem<E>::to_f32(v[j], f);
 #pragma unroll
@@ -354,9 +357,8 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
     };
     for (int it = 0; it < nu; ++it) group(it);
 
-    // ---- the warps' sums meet in shared memory.  Element
-    // g VB + 2 mt + e of a row lies at mt 16 + 2 g + e: neighbouring lanes write
-    // neighbouring words.
+    // ---- the warps' sums meet in shared memory.  What lane g has of m-tile mt lies at
+    // 16 mt + 2 g: neighbouring lanes write neighbouring words.
     constexpr int LD = D + 8;
     __syncthreads();
     float* acc = reinterpret_cast<float*>(smem);
@@ -383,7 +385,8 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
     const int which = begins ? 1 : 0;       // an item begun here and not ended is this CTA's last
     float* part = part_of<D, NT>(a, blockIdx.x, which);
     for (int i = tid; i < t.rows * (D / 2); i += kFThreads) {
-      const int row = i / (D / 2), pr = i % (D / 2), gg = pr / MT, mt = pr % MT, d = gg * VB + 2 * mt;
+      const int row = i / (D / 2), pr = i % (D / 2), d = 2 * pr;
+      const int gg = d % (8 * PW) / PW, mt = d / (8 * PW) * (PW / 2) + d % PW / 2;
       float top = stat[0][row][0];
 #pragma unroll
       for (int k = 1; k < kFWarps; ++k) top = fmaxf(top, stat[k][row][0]);

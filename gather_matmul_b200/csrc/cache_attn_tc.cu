@@ -19,11 +19,15 @@
 //
 // 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1120 us, 920 TFLOP/s,
 // 0.56 of the measured rate of a 16-bit product (a CTA's step 4800 cycles at two tiles).
-// What binds is the data path of shared memory, 128 bytes a cycle, which a step's
-// operands (q and k 1536 cycles, v 512), converted tiles (512), loads (256) and tensor
-// memory traffic (1536) take for 4350.  Measured otherwise: one warpgroup that
-// converts k, then v 1310; scores of 128 tokens at once, which have room for one
-// buffer, 1235; q as an operand from tensor memory, which also leaves room for one, 1370.
+// No unit is full: the tensor pipe is busy 53 % of the time, issue slots 51 %, special
+// functions 32 %.  Scores are there before the softmax asks for them; it forms the
+// weights of 64 tokens in 1250 cycles alone and in up to 2800 beside the other tile's,
+// most of it waiting for shared and tensor memory, which the operands of the products
+// (q and k 1536 cycles of a step, v 512, at 128 bytes a cycle), the converted tiles
+// (512) and the scores and weights themselves keep busy.  Measured otherwise: one
+// warpgroup that converts k, then v 1310; scores of 128 tokens at once, which have room
+// for one buffer, 1235; q as an operand from tensor memory, which leaves room for one
+// buffer of 64, 1370; two softmax warpgroups a tile, half of the columns each, 1255.
 #include <cfloat>
 #include <type_traits>
 

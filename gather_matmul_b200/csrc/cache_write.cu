@@ -8,8 +8,11 @@
 // values are divided by the quotient of the two and rounded once more.
 //
 // Several tokens: one warp holds 16 tokens of one head of k or v in registers (read
-// once), page / 16 warps meet in shared memory for the maximum.  Bound by memory: two
-// bytes read and one written for each element.
+// once), page / 16 warps meet in shared memory for the maximum.  Bound by memory, two
+// bytes read and one written for each element, and by the chain from a slot to its
+// sequence, its page and its scale, which values are loaded beside.  8 x 1024 tokens of
+// 8 heads of 128: 16 us, 3.2 TB/s, 0.48 of the measured copy rate (three CTAs to an SM
+// instead of four 18).  512 single tokens 4.7 us; in the kernel of several 15.
 #include "cache.h"
 #include "common.cuh"
 #include "internal.h"
