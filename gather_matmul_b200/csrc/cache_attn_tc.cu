@@ -61,7 +61,7 @@ template <int D> struct Many {
   // Registers of a thread at launch (checked before the first one), and the shares: the
   // softmax takes what the others give back, no more, and those can only give.
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kSoftRegs = kTiles == 2 ? 136 : 144, kConvRegs = kTiles == 2 ? 72 : 128, kOtherRegs = kTiles == 2 ? 64 : 96;
+  static constexpr int kSoftRegs = kTiles == 2 ? 152 : 144, kConvRegs = kTiles == 2 ? 56 : 128, kOtherRegs = kTiles == 2 ? 56 : 96;
   static_assert(kTiles * kSoftRegs + 2 * kConvRegs + kOtherRegs <= (kTiles + 3) * kLaunchRegs, "more registers than the launch has");
   static_assert(kSoftRegs > kLaunchRegs && kConvRegs <= kLaunchRegs && kOtherRegs < kLaunchRegs, "setmaxnreg in its direction");
   static constexpr int kTileBytes = kN * D * 2;         // 128 rows of fp16

@@ -48,7 +48,7 @@ def _write(L, dt=1, T=8, B=8, H=4, dim=64, page=16, P=100, M=9, k=FAKE, ldk=256,
 SHAPES = [
     (dict(dt=2), INV), (dict(T=-1), INV), (dict(B=-1), INV), (dict(H=0), INV), (dict(dim=0), INV), (dict(page=0), INV),
     (dict(P=0), INV), (dict(M=0), INV), (dict(dim=40), UNS), (dict(dim=272), UNS), (dict(page=24), UNS), (dict(page=8), UNS),
-    (dict(page=256), UNS), (dict(H=4097), UNS), (dict(P=(1 << 22) + 1), UNS), (dict(B=(1 << 16) + 1), UNS), (dict(M=1 << 24), UNS),
+    (dict(page=256), UNS), (dict(H=4097), UNS), (dict(P=(1 << 22) + 1), UNS), (dict(B=(1 << 16) + 1), UNS), (dict(M=1 << 24), UNS), (dict(M=1 << 23), UNS),
     (dict(T=7), INV),                                    # without starts, a row for each sequence
     (dict(T=(1 << 22) + 1, starts=FAKE), UNS),
     (dict(cache=0), INV), (dict(scale=0), INV), (dict(tables=0), INV), (dict(lengths=0), INV), (dict(work=0), INV),

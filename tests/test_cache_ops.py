@@ -289,6 +289,76 @@ def test_a_nan_scale_spoils_its_head_alone(news):
     assert nan[1:, 2:].all() and not nan[:1].any() and not nan[:, :2].any()
 
 
+@pytest.mark.parametrize("group", [100, 256, 300, 700])
+def test_one_head_of_k_for_hundreds_of_q(group):
+    c = Cache([333, 0, 70], 1, 64, 16, seed=group)
+    q = rows(c.B, group * 64, BF16, gen(25))
+    attend(c, q, torch.full_like(q, math.nan), None)
+    q = rows(5, group * 64, F16, gen(26))
+    attend(c, q, torch.full_like(q, math.nan), [2, 0, 3])
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("news", [None, [30, 1]], ids=["single", "chunks"])
+def test_a_query_of_no_number_spoils_its_row_alone(what, news):
+    c = Cache([500, 90], 2, 64, 16, seed=27)
+    T = 2 if news is None else sum(news)
+    q, starts = rows(T, 4 * 64, BF16, gen(27)), None if news is None else starts_of(news)
+    y, z = torch.empty_like(q), torch.empty_like(q)
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=starts)
+    q[0, 70] = what                                          # head 1 of the first token
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts)
+    assert z[0, 64:128].isnan().all()
+    z[0, 64:128] = y[0, 64:128]
+    assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("what", [0x7F, 0xFF])
+@pytest.mark.parametrize("news", [None, [40, 30]], ids=["single", "chunks"])
+def test_values_behind_the_last_token_may_be_anything(what, news):
+    """NaN there, in the places of the last page and in pages that are held and not needed."""
+    c = Cache([83, 33], 2, 128, 16, seed=28, spare=8, more_places=3)
+    q, starts = rows(2 if news is None else sum(news), 4 * 128, F16, gen(28)), None if news is None else starts_of(news)
+    y, z = torch.empty_like(q), torch.empty_like(q)
+    for b, n in enumerate(c.lens):
+        c.cache[int(c.tables[b, n // 16]), :, :, n % 16:] = 0.0
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=starts)
+    for b, n in enumerate(c.lens):
+        c.cache.view(torch.uint8)[int(c.tables[b, n // 16]), :, :, n % 16:] = what
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts)
+    assert torch.equal(y, z) and torch.isfinite(y).all()
+
+
+def test_offsets_past_32_bits():
+    """A cache of 5 GB whose last pages are in use, written, read and moved."""
+    P, H, page, dim = 40000, 8, 64, 128
+    c = Cache([1], H, dim, page)
+    c.cache = torch.zeros(P, 2, H, page, dim, dtype=torch.uint8, device="cuda").view(FP8)
+    assert c.cache.numel() > 1 << 32
+    c.scale, c.P, c.B, c.M = torch.ones(P, 2, H, device="cuda"), P, 3, 4
+    c.tables = ints([[P - 1, P - 3, P - 2, -1], [P - 4, -1, -1, -1], [P - 5, P - 6, -1, -1]])
+    c.refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+    c.refs[P - 6:] = 1
+    c.lens, c.work = [150, 1, 100], ops.cache_workspace(P, dim)
+    c.lengths = ints(c.lens)
+    x = rows(251, 2 * H * dim, BF16, gen(29))
+    ops.cache_write(x[:, :H * dim], x[:, H * dim:], c.cache, c.scale, c.tables, c.lengths, c.work, starts=starts_of(c.lens))
+    c.lens = [151, 2, 101]
+    c.lengths += 1
+    ops.cache_write(x[:3, :H * dim], x[:3, H * dim:], c.cache, c.scale, c.tables, c.lengths, c.work)
+    k, v = c.kv(0, 5)
+    assert (k[:150] - x[:150, 5 * dim:6 * dim].double()).abs().max() <= 2.0 ** -4 * 8 and k.abs().max() > 1
+    for news in (None, [40, 2, 9]):
+        q = rows(3 if news is None else sum(news), 2 * H * dim, BF16, gen(30))
+        attend(c, q, torch.full_like(q, math.nan), news)
+    y, z = torch.empty_like(q[:3]), torch.empty_like(q[:3])
+    ops.cache_attention(q[:3], c.cache, c.scale, c.tables, c.lengths, y, c.work)
+    ops.pages_compact(c.tables, c.refs, c.cache[None], c.scale[None], c.work)
+    assert sorted(c.tables[c.tables >= 0].tolist()) == [0, 1, 2, 3, 4, 5]
+    ops.cache_attention(q[:3], c.cache, c.scale, c.tables, c.lengths, z, c.work)
+    assert torch.equal(y, z) and c.errors() == _lib.LORA_OK
+
+
 @pytest.mark.parametrize("entry", [-1, 10 ** 6, -2 ** 31])
 @pytest.mark.parametrize("news", [None, [1, 40]], ids=["single", "chunks"])
 def test_a_missing_page_is_left_out_and_counted(entry, news):
