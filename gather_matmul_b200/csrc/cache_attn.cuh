@@ -83,7 +83,8 @@ __device__ __forceinline__ void tile_of(const AttnArgs& a, int b, int64_t slot, 
 struct Shared {
   unsigned long long warp[32];
   int slot, seq;
-  unsigned long long off, all;
+  unsigned long long off;
+  int real;                                   // units of this CTA's share that have tokens
   int flag;
 };
 
@@ -113,6 +114,7 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
     if (lane >= d) in += v;
   }
   if (lane == 31) sm.warp[warp] = in;
+  if (threadIdx.x == 0) sm.real = 0;
   __syncthreads();
   unsigned long long base = 0;
   all = 0;
@@ -128,21 +130,28 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
     w1 = all * (blockIdx.x + 1) / ctas;
   }
   const unsigned long long begin = base + in - mine;
-  if (w0 < w1 && begin <= w0 && w0 < begin + mine) {
+  if (begin < w1 && w0 < begin + mine) {
     unsigned long long at = begin;
+    int real = 0;
     b = first;
-    for (int64_t s = s0; s < s1; ++s) {
+    for (int64_t s = s0; s < s1 && at < w1; ++s) {
       while (b + 1 < a.B && slot_of<R>(a, b + 1) <= s) ++b;
       tile_of<R, U, C>(a, b, s, t);
       const unsigned long long u = (unsigned long long)t.units * a.Hk;
       if (w0 < at + u) {
-        sm.slot = (int)s;
-        sm.seq = b;
-        sm.off = w0 - at;
-        break;
+        if (w0 >= at) {
+          sm.slot = (int)s;
+          sm.seq = b;
+          sm.off = w0 - at;
+        }
+        // idle units before place x of the slot
+        const auto idle = [&](unsigned long long x) { return (int)(x / t.units) * C + (int)min((unsigned long long)C, x % t.units); };
+        const unsigned long long from = max(w0, at) - at, to = min(w1, at + u) - at;
+        real += (int)(to - from) - (idle(to) - idle(from));
       }
       at += u;
     }
+    atomicAdd(&sm.real, real);
   }
   __syncthreads();
 }

@@ -51,6 +51,7 @@ constexpr float kNothing = 0x1p-60f;
 constexpr uint32_t kPolyPairs = 0x12;
 constexpr int kBlock = 4, kBlocks = 4;        // steps that are planned at once, and such blocks in shared memory
 constexpr int kRing = kBlock * kBlocks;
+constexpr int kIdle = 3;                      // what an item costs beside its steps, in steps
 
 template <int D> struct Many {
   static constexpr int kTiles = D <= 128 ? 2 : 1;
@@ -93,7 +94,7 @@ struct Item {
 struct ManyShared {
   Shared div;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], o_empty[2], plan_full[kBlocks], plan_empty[kBlocks], done[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], o_empty[2], plan_items[kBlocks], plan_full[kBlocks], plan_empty[kBlocks], done[2];
   uint32_t tmem;
   int stop;
   int flag[2];
@@ -112,22 +113,27 @@ struct Cursor {
   template <int R>
   __device__ __forceinline__ bool next(const AttnArgs& a) {
     if (w >= w1) return false;
-    for (;;) {
-      while (seq + 1 < a.B && slot_of<R>(a, seq + 1) <= slot) ++seq;
-      tile_of<R, kN, 0>(a, seq, slot, t);
-      const unsigned long long slot_units = (unsigned long long)t.units * a.Hk;
-      if (off < slot_units) break;
-      off -= slot_units;
-      ++slot;
-    }
-    h = (int)(off / t.units);
-    ua = (int)(off - (unsigned long long)h * t.units);
-    nu = (int)min((unsigned long long)(t.units - ua), w1 - w);
-    item0 = w - ua;
-    item1 = item0 + t.units;
-    w += nu;
-    off += nu;
-    return true;
+    do {
+      for (;;) {
+        while (seq + 1 < a.B && slot_of<R>(a, seq + 1) <= slot) ++seq;
+        tile_of<R, kN, kIdle>(a, seq, slot, t);
+        const unsigned long long slot_units = (unsigned long long)t.units * a.Hk;
+        if (off < slot_units) break;
+        off -= slot_units;
+        ++slot;
+      }
+      h = (int)(off / t.units);
+      const int from = (int)(off - (unsigned long long)h * t.units);
+      const int share = (int)min((unsigned long long)(t.units - from), w1 - w);
+      // of the units that have tokens
+      ua = max(from - kIdle, 0);
+      nu = from + share - kIdle - ua;
+      item0 = w - from + kIdle;
+      item1 = w - from + t.units;
+      w += share;
+      off += share;
+    } while (nu <= 0 && w < w1);
+    return nu > 0;
   }
 };
 
@@ -232,6 +238,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       ptx::mbar_init(&sm.o_empty[i], 4);
     }
     for (int i = 0; i < kBlocks; ++i) {
+      ptx::mbar_init(&sm.plan_items[i], 1);
       ptx::mbar_init(&sm.plan_full[i], 1);
       ptx::mbar_init(&sm.plan_empty[i], 4 * (M::kTiles + 2));
     }
@@ -245,10 +252,10 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
   ptx::tc_fence_before();
   unsigned long long w0, w1, all;
   int ctas;
-  divide<M::kRows, kN, 0>(a, sm.div, 2, w0, w1, all, ctas);   // __syncthreads
+  divide<M::kRows, kN, kIdle>(a, sm.div, 2, w0, w1, all, ctas);   // __syncthreads
   ptx::tc_fence_after();
   const uint32_t tmem = same(sm.tmem);
-  const int steps = same((int)(w1 - w0));
+  const int steps = same(sm.div.real);
   const uint32_t s_col = 0, o_col = M::kTiles * kN;
 
   if (wg < M::kTiles) {
@@ -269,7 +276,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     // the next item in which this tile has rows, or -1
     auto seek = [&]() -> int {
       while (st < steps) {
-        planned();
+        ptx::mbar_wait_asm(ptx::smem_u32(&sm.plan_items[st / kBlock % kBlocks]), (st / kRing) & 1, stop);
         const int item = same(sm.step[st % kRing].item);
         if (same(sm.item[item].rows) > 128 * tile) return item;
         for (int n = same(sm.item[item].steps); n > 0; --n) {
@@ -780,7 +787,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
               it.first_cta = owner(cur.item0, all, ctas);
               it.last_cta = owner(cur.item1 - 1, all, ctas);
               // begun here and not ended: this CTA's last
-              it.which = cur.nu == cur.t.units ? -1 : (cur.ua == 0 ? 1 : 0);
+              it.which = cur.nu == cur.t.units - kIdle ? -1 : (cur.ua == 0 ? 1 : 0);
             }
           }
           const int tok = (cur.t.u0 + cur.ua + u) * kN;
@@ -796,6 +803,8 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
             step.item = item;
           }
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.plan_items[block]);       // q can be fetched meanwhile
         int64_t where = -1;
         float4 scale = make_float4(1.f, -INFINITY, 0.f, 0.f);         // weights of 0, for scores of -inf too
         if (entry >= 0) {
