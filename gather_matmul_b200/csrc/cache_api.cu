@@ -182,11 +182,20 @@ lora_status lora_cache_attention(lora_dtype dtype, int T, int n_seqs, int q_head
   a.window = window;
   a.c = (float)((double)softmax_scale * 1.4426950408889634);
   cudaGetLastError();
-  // Sequences of up to kFewRows rows and others go to kernels of their own.  Only
-  // the device knows them where starts is given, so both are launched then, but
-  // where all rows are few, or are those of one sequence.
-  const int rows = starts ? (int)min((int64_t)T * a.group, (int64_t)INT_MAX) : a.group;
-  const bool few = rows <= kFewRows || (starts && n_seqs > 1), many = rows > kFewRows;
+  // Sequences of up to kFewRows rows and others have kernels of their own; only the device
+  // knows them where starts is given.  The kernel for many rows takes all, at less than
+  // half the speed for few; a second launch costs 20 us, most of it the kernel's way to
+  // its first products.  Items (sequences x k/v heads) are what the host knows:
+  //   up to 128, one for each CTA at most: one kernel.  12 sequences of up to 8 tokens over
+  //     12 000 on 4 heads 43 us, in two kernels 75; 16 of up to 200 over 2000 38 and 60;
+  //     36 of up to 4 over 30 000 (144 items) 99 and 91
+  //   up to 8 for each CTA: one, unless the rows say that most sequences are short.  64 of
+  //     up to 200 over 8000 94 us and 122; 64 of up to 4 over 8000 66 and 61
+  //   more: two.  300 of up to 16 over 8000 on 8 heads 326 us and 305; 150 of up to 64
+  //     (1200 items) 218 and 220
+  const int64_t rows = starts ? (int64_t)T * a.group : a.group, items = (int64_t)n_seqs * kv_heads;
+  const bool one = !starts || items <= 128 || (items <= 8 * 148 && rows > (int64_t)kFewRows * n_seqs);
+  const bool many = rows > kFewRows, few = !many || !one;
   cudaError_t e = cudaSuccess;
   if (many) {
     a.min_rows = few ? kFewRows + 1 : 1;

@@ -191,6 +191,24 @@ def test_ragged_chunks(dtype, dim, page, H, group, window):
     attend(c, q, torch.full_like(q.contiguous(), math.nan), news, window=window)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 176, 256])
+@pytest.mark.parametrize("B,H,group", [(70, 2, 2), (400, 3, 16), (300, 4, 3)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_batches_for_both_kernels(dtype, dim, B, H, group, window):
+    """Many sequences, most of them of few rows, some longer, some empty: each kernel takes its own."""
+    g = torch.Generator().manual_seed(B + dim)
+    news = [int(v) for v in torch.randint(0, 3, (B,), generator=g)]
+    news[3], news[B // 2], news[B - 1] = (20, 16 // group, 7) if group == 16 else (200, 16 // group + 1, 90)
+    lens = [n + int(v) if i % 5 else n for i, (n, v) in enumerate(zip(news, torch.randint(0, 150, (B,), generator=g)))]
+    c = Cache(lens, H, dim, 16, seed=B)
+    q = rows(sum(news), H * group * dim, dtype, gen(31))
+    assert B * H > 128 and (B * H > 8 * 148 or sum(news) * group <= 16 * B)
+    before = ops.launch_count()
+    attend(c, q, torch.full_like(q, math.nan), news, window=window)
+    assert ops.launch_count() - before == 2
+
+
 @pytest.mark.parametrize("window", [1, 16, 64, 100, 5000])
 @pytest.mark.parametrize("news", [None, [3, 200, 1, 65]], ids=["single", "chunks"])
 def test_windows(window, news):
