@@ -17,8 +17,8 @@
 //   a warp for each tile that issues its products, and one that plans: it looks up
 //     pages and scales of the next steps, four steps at a time, and divides the items
 //
-// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1120 us, 920 TFLOP/s,
-// 0.56 of the measured rate of a 16-bit product (a CTA's step 4800 cycles at two tiles).
+// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1100 us, 937 TFLOP/s,
+// 0.57 of the measured rate of a 16-bit product (a CTA's step 4800 cycles at two tiles).
 // No unit is full: the tensor pipe is busy 53 % of the time, issue slots 51 %, special
 // functions 32 %.  Scores are there before the softmax asks for them; it forms the
 // weights of 64 tokens in 1250 cycles alone and in up to 2800 beside the other tile's,
@@ -51,7 +51,10 @@ constexpr float kNothing = 0x1p-60f;
 constexpr uint32_t kPolyPairs = 0x12;
 constexpr int kBlock = 4, kBlocks = 4;        // steps that are planned at once, and such blocks in shared memory
 constexpr int kRing = kBlock * kBlocks;
-constexpr int kIdle = 3;                      // what an item costs beside its steps, in steps
+// What an item costs beside its steps, in steps (q in, results out, the first scores:
+// 9 us).  37 chunks and tokens with a window, and the case above: 1 step 92 and 1102 us,
+// 3 90 and 1100, 5 92 and 1094.
+constexpr int kIdle = 3;
 
 template <int D> struct Many {
   static constexpr int kTiles = D <= 128 ? 2 : 1;
