@@ -90,7 +90,8 @@ struct Shared {
 
 // This CTA's share [w0, w1) of all units, and the first one's slot, sequence and
 // place among the slot's units (of all k/v heads).  Every thread calls it.  CTAs
-// past `ctas` get nothing.
+// past `ctas` get nothing, and none does where starts descend: a slot's sequence is
+// found by bisection here and by walking on elsewhere, which agree in ascending starts.
 template <int R, int U, int C>
 __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_units, unsigned long long& w0,
                                        unsigned long long& w1, unsigned long long& all, int& ctas) {
@@ -115,13 +116,22 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
   }
   if (lane == 31) sm.warp[warp] = in;
   if (threadIdx.x == 0) sm.real = 0;
-  __syncthreads();
+  bool descends = false;
+  if (a.starts != nullptr && (!one_tile<R>() || blockIdx.x == 0)) {
+    for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
+      const int q0 = a.starts[i], q1 = a.starts[i + 1];
+      descends |= q1 < q0;
+      if (blockIdx.x == 0 && (q0 < 0 || q1 < q0 || q1 > a.T)) atomicAdd(a.bad + 1, 1);
+    }
+  }
+  descends = __syncthreads_or(descends) && !one_tile<R>();
   unsigned long long base = 0;
   all = 0;
   for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
     if (i == warp) base = all;
     all += sm.warp[i];
   }
+  if (descends) all = 0;
   ctas = (int)min((unsigned long long)gridDim.x, max(all / min_units, 1ull));
   if ((int)blockIdx.x >= ctas) {
     w0 = w1 = 0;

@@ -546,7 +546,8 @@ LORA_API lora_status lora_norm_rope(lora_dtype dtype, int T, int head_dim, int r
  *            sequence b are rows starts[b] .. starts[b+1] of the call's tensors,
  *            the last ones of its length; rows from starts[n_seqs] on are neither
  *            read nor written.  NULL: row b is the one new token of sequence b
- *            (then T = n_seqs).
+ *            (then T = n_seqs).  Where starts descend, the attention of the call's
+ *            sequences is left out, in whole or in part, and counted.
  *   work     device workspace of lora_cache_workspace_bytes(n_pages, head_dim),
  *            256-byte aligned, zero-filled once before its first use; it serves
  *            every call on a cache of that many pages.  Calls that may run at

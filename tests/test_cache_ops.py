@@ -431,6 +431,30 @@ def test_starts_out_of_order_stay_in_bounds(starts):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("group", [1, 4])
+def test_descending_starts_of_many_rows_end_and_are_counted(group):
+    """Sequences of many tiles, whose places a bisection and a walk would not agree on."""
+    B, T = 12, 4000
+    c = Cache([900] * B, 2, 64, 16)
+    whole = torch.full((T + 32, 2 * group * 64), 3.0, dtype=BF16, device="cuda")
+    q, y = rows(T, 2 * group * 64, BF16, gen(20)), whole[16:T + 16]
+    order = [0, 500, 100, 700, 300, 2000, 900, 3100, 1500, 3900, 2500, 4000, 3300]
+    for starts in (order, order[::-1], [0, 2, 1, 3, 2, 4, 3, 5, 4, 4000, 10, 4000, 0]):
+        ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=ints(starts))
+        torch.cuda.synchronize()
+        assert ops.check_errors(c.work) == _lib.LORA_ERR_BAD_INDEX
+        assert (whole[:16] == 3).all() and (whole[T + 16:] == 3).all()
+        # the workspace is as it was: a good call's results hold
+        news = [9] * B
+        z = torch.empty(9 * B, 2 * group * 64, dtype=BF16, device="cuda")
+        ops.cache_attention(q[:9 * B], c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts_of(news))
+        assert ops.check_errors(c.work) == _lib.LORA_OK
+        one = torch.empty_like(z)
+        ops.cache_attention(q[:9 * B], c.cache, c.scale, c.tables, c.lengths, one,
+                            ops.cache_workspace(c.cache.shape[0], 64), starts=starts_of(news))
+        assert torch.equal(z, one)
+
+
 # ---------------------------------------------------------------- the write
 def grid():
     return torch.tensor([m * 2.0 ** -9 for m in range(8)] +
