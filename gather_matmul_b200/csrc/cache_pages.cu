@@ -32,7 +32,8 @@ struct PlanShared {
 };
 
 // Exclusive ranks of two counts over the cluster's threads in order, and the
-// totals.  Every thread of the cluster calls it.
+// totals.  Every thread of the cluster calls it, once it knows that the cluster's
+// CTAs have all begun: their shared memory is written.
 __device__ __forceinline__ void cluster_ranks(PlanShared& sm, int2 mine, int2& before, int2& total) {
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -112,6 +113,7 @@ __device__ __forceinline__ void lacking(const PagePlanArgs& a, int b, int& held,
 
 __global__ void __launch_bounds__(kPThreads) pages_extend_kernel(const __grid_constant__ PagePlanArgs a) {
   __shared__ PlanShared sm;
+  ptx::cluster_arrive();
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
   int p0, p1, b0, b1;
@@ -122,6 +124,8 @@ __global__ void __launch_bounds__(kPThreads) pages_extend_kernel(const __grid_co
     lacking(a, b, held, need);
     want += need - held;
   }
+  __syncwarp();
+  ptx::cluster_wait();
   int2 before, total;
   cluster_ranks(sm, make_int2(count_free(a.refs, p0, p1), want), before, total);
   if (total.y == 0) return;                     // the same for the whole cluster
@@ -264,12 +268,15 @@ __global__ void __launch_bounds__(kPThreads) pages_fork_kernel(const __grid_cons
 // at n or above, which are cleared after everyone has read them.
 __global__ void __launch_bounds__(kPThreads) pages_compact_kernel(const __grid_constant__ PagePlanArgs a) {
   __shared__ PlanShared sm;
+  ptx::cluster_arrive();
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
   cg::cluster_group cl = cg::this_cluster();
   int p0, p1;
   share_of(a.P, p0, p1);
   const int live = p1 - p0 - count_free(a.refs, p0, p1);
+  __syncwarp();
+  ptx::cluster_wait();
   int2 before, total;
   cluster_ranks(sm, make_int2(live, 0), before, total);
   const int n = total.x;
