@@ -34,10 +34,11 @@ lora_status check_cache(int pages, int kv_heads, int page_tokens, int dim) {
   return LORA_OK;
 }
 
-// tables of n sequences of up to m pages
+// tables of n sequences of up to m pages; ranks of places are 32-bit numbers
 lora_status check_seqs(int n, int m) {
   if (n < 0 || m <= 0) return LORA_ERR_INVALID_ARG;
-  if (n > LORA_MAX_SEQS || (int64_t)m * 128 > INT_MAX / 2) return LORA_ERR_UNSUPPORTED;
+  if (n > LORA_MAX_SEQS || (int64_t)m * 128 > INT_MAX / 2 || (int64_t)n * m > INT_MAX)
+    return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 

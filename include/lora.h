@@ -555,7 +555,7 @@ LORA_API lora_status lora_norm_rope(lora_dtype dtype, int T, int head_dim, int r
  *
  * page_tokens is 16, 32, 64 or 128, head_dim a multiple of 16 up to
  * LORA_MAX_HEAD_DIM, n_pages at most LORA_MAX_PAGES, n_seqs at most
- * LORA_MAX_SEQS, max_pages * 128 below 2^30.
+ * LORA_MAX_SEQS, max_pages * 128 below 2^30, n_seqs * max_pages below 2^31.
  * A table entry that is no page where one is needed, and whatever else only the
  * device can see to be wrong, is left out and counted in the workspace:
  * lora_check_errors(work, ...) then returns LORA_ERR_BAD_INDEX.  The lists that a

@@ -128,6 +128,15 @@ def test_page_refusals(L, call, kw, status):
     assert call(L, **kw) == status
 
 
+@pytest.mark.parametrize("call", [_write, _attend, _extend, _free, _fork, _compact])
+def test_tables_of_more_places_than_ranks_have(call, L):
+    assert call(L, B=1 << 10, M=1 << 21, **(dict(T=1 << 10) if call in (_write, _attend) else {})) == UNS
+    assert call(L, B=1 << 16, M=1 << 15, **(dict(T=1 << 16) if call in (_write, _attend) else {})) == UNS
+    # one place fewer is refused for what comes next
+    small = dict(T=1 << 10, work=FAKE + 128) if call in (_write, _attend) else dict(work=FAKE + 64)
+    assert call(L, B=1 << 10, M=(1 << 21) - 1, **small) == MIS
+
+
 def test_binding_refusals_on_cpu_tensors():
     P, H, page, dim, B, M = 10, 2, 16, 64, 3, 4
     cache, scale = torch.zeros(P, 2, H, page, dim).to(torch.float8_e4m3fn), torch.ones(P, 2, H)
