@@ -85,8 +85,11 @@ struct Step {
   int item;
 };
 constexpr uint32_t kFirst = 1, kLast = 2, kSecond = 4;
-// What the softmax needs to know of an item.  A slot is written again kItems items
-// later, when the softmax has long passed all steps of the first one.
+// What the softmax needs to know of an item.  The plan is at most kRing steps ahead of
+// what each softmax has passed, so an item's slot, written again kItems items later, holds
+// it until its steps are passed.  Its results come later still: the second tile's softmax
+// passes the steps of all items without rows for it before it writes them.  What an item's
+// steps and results need is in the tile's own copy.
 constexpr int kItems = 2 * kRing;
 struct Item {
   int q0, r0, rows, base;                     // row r: query q0 + r / group, at position base + r / group
@@ -104,6 +107,7 @@ struct ManyShared {
   float q_scale[2][128];                      // of a tile's rows
   Step step[kRing];
   Item item[kItems];
+  Item own[2];                                // the one that a tile's softmax is at
 };
 
 // The items of a CTA's share, one after another.
@@ -358,6 +362,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
           if (piece == 0) sm.q_scale[tile][at] = __uint_as_float((uint32_t)(127 - n) << 23);
         }
       }
+      if (row == 0) sm.own[tile] = sm.item[item];
       ptx::fence_proxy_async_smem();
       tile_sync(tile);
       cs = sm.q_scale[tile][row];
@@ -369,10 +374,9 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       put_q(item);
     }
     while (item >= 0) {
-      const int now = item;
+      const Item& it = sm.own[tile];
       int pos, pos_low, pos_high, tok, n_steps;
       {
-        const Item& it = sm.item[now];
         pos = 128 * tile + row < it.rows ? it.base + (it.r0 + 128 * tile + row) / a.group : -1;
         pos_low = same(it.base + (it.r0 + 128 * tile) / a.group);
         pos_high = same(it.base + (it.r0 + min(it.rows, 128 * tile + 128) - 1) / a.group);
@@ -499,7 +503,6 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       ptx::mbar_wait_asm(ptx::smem_u32(&sm.o_full[tile][1]), (n_s + 1) & 1, stop);   // the last half's products
       ptx::tc_fence_after();
       // the thread's row, into the place of q
-      const Item& it = sm.item[now];
       const int which = same(it.which);
       auto put = [&](int j, const float* o) {
 #pragma unroll
