@@ -247,7 +247,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     for (int i = 0; i < kBlocks; ++i) {
       ptx::mbar_init(&sm.plan_items[i], 1);
       ptx::mbar_init(&sm.plan_full[i], 1);
-      ptx::mbar_init(&sm.plan_empty[i], 4 * (M::kTiles + 2));
+      ptx::mbar_init(&sm.plan_empty[i], 4 * (M::kTiles + 2) + M::kTiles);   // softmax and conversion, issuing warps
     }
     ptx::mbar_init(&sm.done[0], 1);
     ptx::mbar_init(&sm.done[1], 1);
@@ -665,7 +665,15 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       uint32_t n_q = 0, n_p = 0, n_o = 0;
       auto flags = [&](int st) -> uint32_t {
         ptx::mbar_wait_asm(ptx::smem_u32(&sm.k_full[st % M::kBufs]), (st / M::kBufs) & 1, stop);
-        return same(sm.step[st % kRing].flags);
+        const uint32_t f = same(sm.step[st % kRing].flags);
+        // the block is written again when this warp has read it too: nothing else says so
+        // in steps without rows for its tile
+        if (st % kBlock == kBlock - 1) {
+          __syncwarp();
+          if (one) ptx::mbar_arrive(&sm.plan_empty[st / kBlock % kBlocks]);
+          __syncwarp();
+        }
+        return f;
       };
       auto scores = [&](auto half, int st, uint32_t f) {
         constexpr int h = decltype(half)::value;

@@ -48,3 +48,22 @@ def test_many_small_items_behind_a_large_one(batch, dim, dtype):
     d.work = c.work
     q = rows(300, H * group * dim, dtype, gen(42))
     attend(d, q, torch.full_like(q, math.nan), [290, 10])
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, F16)])
+def test_thousands_of_steps_without_a_second_tile(dim, dtype):
+    """Most items have rows for one tile only, now and then one has for both: the warp that issues the
+    second tile's products runs through the plan with nothing to wait for but the keys."""
+    r = random.Random(45)
+    news = [r.randint(20, 32) if i % 23 else r.randint(65, 80) for i in range(700)]
+    lens = [n + r.randint(0, 600) for n in news]
+    c = Cache(lens, 4, dim, 32, seed=45)
+    q = rows(sum(news), 16 * dim, dtype, gen(45))
+    y = torch.full_like(q, math.nan)
+    attend(c, q, y, news)
+    starts = starts_of(news)
+    for _ in range(10):
+        z = torch.full_like(q, math.nan)
+        ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts)
+        assert torch.equal(y, z)
+    assert c.errors() == _lib.LORA_OK
