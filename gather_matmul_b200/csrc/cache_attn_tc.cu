@@ -76,7 +76,7 @@ template <int D> struct Many {
 
 // What the other roles need to know of a step, by groups of 16 tokens (which lie
 // in one page): where a group's k begins in the cache (negative: nowhere, or not
-// visible), and (k scale * c, log2 v scale, 1 / v scale).
+// visible), and (k scale, log2 v scale, 1 / v scale).
 struct Step {
   float4 scale[8];
   int64_t at[8];
@@ -365,7 +365,10 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       if (row == 0) sm.own[tile] = sm.item[item];
       ptx::fence_proxy_async_smem();
       tile_sync(tile);
-      cs = sm.q_scale[tile][row];
+      // The factor of a score is a page's (at least 2^-32) times this one.  It stays off zero,
+      // since masked scores are -inf before it: a row of zeros has the scale 2^-120.  Where
+      // the bound is met the scores are below 2^-30, and no weight changes.
+      cs = fmaxf(sm.q_scale[tile][row] * a.c, 0x1p-90f);
       warp_arrive(&sm.q_full[tile], lane);
     };
     int item = seek();
@@ -828,7 +831,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
           } else {
             const int64_t page = (int64_t)pid * 2 * a.Hk + head;
             const float ks = a.scale[page], vs = a.scale[page + a.Hk];
-            scale = make_float4(ks * a.c, log2f(vs), 1.f / vs, 0.f);
+            scale = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
             where = page * head_bytes + (int64_t)(at & ((1 << a.page_log) - 1)) * a.dim;
           }
         }

@@ -9,6 +9,7 @@ import torch
 
 from gather_matmul_b200 import _lib, ops
 from test_cache_ops import BF16, F16, Cache, attend, gen, rows, starts_of
+from test_cache_paths import Model
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,34 @@ def test_thousands_of_steps_without_a_second_tile(dim, dtype):
         ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts)
         assert torch.equal(y, z)
     assert c.errors() == _lib.LORA_OK
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("softmax_scale", [None, 1e-20, 3.0])
+@pytest.mark.parametrize("news", [None, [300, 7, 1, 64]], ids=["single", "chunks"])
+def test_zeros_give_the_mean_of_the_values(news, softmax_scale, dim):
+    """Rows of zeros over keys of zeros, whose factors are the smallest there are: every score is 0, masked or not."""
+    c = Cache([300, 500, 129, 64], 2, dim, 16, seed=43)
+    held = c.refs.bool()
+    c.cache.view(torch.uint8)[held, 0] = 0
+    c.scale[held, 0] = 2.0 ** -32
+    T = 4 if news is None else sum(news)
+    q = torch.zeros(T, 4 * dim, dtype=BF16, device="cuda")
+    attend(c, q, torch.full_like(q, math.nan), news, softmax_scale=softmax_scale)
+    q[::3] = rows(len(q[::3]), 4 * dim, BF16, gen(43))        # some rows of numbers among them
+    attend(c, q, torch.full_like(q, math.nan), news, softmax_scale=softmax_scale)
+    attend(c, q, torch.full_like(q, math.nan), news, softmax_scale=softmax_scale, window=50)
+
+
+def test_a_layer_s_step_on_zeros_gives_zeros():
+    """As a server warms up: x = 0 gives q = k = v = 0."""
+    m = Model(1, 8, 2, 128, 16, 64, 3, 12, seed=9)
+    news = [100, 3, 40]
+    m.lengths += torch.tensor(news, dtype=torch.int32, device="cuda")
+    m.extend()
+    T = sum(news)
+    buf = m.buffers(T)
+    m.run(torch.zeros(T, m.K, dtype=m.dtype, device="cuda"), torch.full((T,), -1, dtype=torch.int32, device="cuda"),
+          torch.arange(T, device="cuda"), buf, starts_of(news))
+    assert (buf[0][0] == 0).all() and (buf[0][1] == 0).all()
+    assert ops.check_errors(m.work) == _lib.LORA_OK
