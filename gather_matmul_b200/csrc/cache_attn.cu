@@ -291,13 +291,22 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
           }
         }
       }
-      const float ks = r.ks, lv = log2_fast(r.vs), inv = inverse_fast(r.vs);
+      const float ks = r.ks, lv = log2_fast(r.vs);
+      float inv = inverse_fast(r.vs);
       load_k(r, it + 1);                 // (r.at is the next group's from here on)
       if (!have) {
         load_v(r, it + 1);
         return;
       }
       const bool edge = tok + 15 > pos_low || (a.window > 0 && tok <= pos_high - a.window);
+      // A NaN scale spoils the rows that see its page and no others: their weights of 0 meet
+      // numbers, in the denominator and in the product.  (On every group, edge or not, it
+      // cost the decode batch 2 %.)
+      if (edge && lv != lv) {
+        inv = 1.f;
+#pragma unroll
+        for (int j = 0; j < VB / 4; ++j) r.v[0][j] = r.v[1][j] = r.v[2][j] = r.v[3][j] = 0;
+      }
       uint32_t p[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {

@@ -75,11 +75,15 @@ template <int D> struct Many {
 };
 
 // What the other roles need to know of a step, by groups of 16 tokens (which lie
-// in one page): where a group's k begins in the cache (negative: nowhere, or not
-// visible), and (k scale, log2 v scale, 1 / v scale).
+// in one page): where a group's k and v begin in the cache behind their first page
+// (kNowhere: no page, or not visible; kNaN), and (k scale, log2 v scale, 1 / v scale).
+// A page whose k or v scale is NaN spoils the rows that see it and no others: its k are
+// read as NaN, which masks take out of a score, its v as zeros and its scales as 1, so
+// that weights of 0 add nothing.
+constexpr int64_t kNowhere = -1, kNaN = -2;
 struct Step {
   float4 scale[8];
-  int64_t at[8];
+  int64_t at[2][8];
   int visible;                                // tokens of the step below the last visible one
   uint32_t flags;                             // kFirst, kLast: of its item here; kSecond: so has the second tile rows
   int item;
@@ -186,13 +190,13 @@ __device__ __forceinline__ void exp2_fma(float& x, float& y) {
       : "=f"(x), "=f"(y) : "r"(nx), "r"(ny), "l"(p));
 }
 
-// 16 bytes, or zeros: no branch, so that the loads of a loop follow one another
-__device__ __forceinline__ uint4 load_if(const void* p, bool in) {
+// 16 bytes, or what stands for them: no branch, so that the loads of a loop follow one another
+__device__ __forceinline__ uint4 load_if(const void* p, bool in, uint32_t other = 0) {
   uint4 v;
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, %6;\n mov.b32 %1, %6;\n mov.b32 %2, %6;\n mov.b32 %3, %6;\n"
       " @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)in));
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)in), "r"(other));
   return v;
 }
 // One arrival for the warp: hundreds of them a step, each a write to shared memory,
@@ -621,11 +625,12 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       const int visible = is_v ? step.visible : kN;         // v behind the last visible token may be
 #pragma unroll                                              // anything: zeros in its place
       for (int g = 0; g < 4; ++g) {
-        const int64_t at = step.at[2 * g + (row0 >> 4)];
+        const int64_t at = step.at[is_v][2 * g + (row0 >> 4)];
         const uint8_t* src = base + at + lane_at;
         const bool in = at >= 0 && row0 + 32 * g < visible;
+        const uint32_t other = at == kNaN ? 0x7f7f7f7fu : 0u;
 #pragma unroll
-        for (int c = 0; c < A; ++c) r[g * A + c] = load_if(src + 64 * c, in && e0 + 64 * c < a.dim);
+        for (int c = 0; c < A; ++c) r[g * A + c] = load_if(src + 64 * c, in && e0 + 64 * c < a.dim, other);
       }
       // this step's entries are not looked at again
       if (st % kBlock == kBlock - 1) {
@@ -822,7 +827,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.plan_items[block]);       // q can be fetched meanwhile
-        int64_t where = -1;
+        int64_t k_where = kNowhere, v_where = kNowhere;
         float4 scale = make_float4(1.f, -INFINITY, 0.f, 0.f);         // weights of 0, for scores of -inf too
         if (entry >= 0) {
           const int pid = a.tables[entry];
@@ -831,14 +836,20 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
           } else {
             const int64_t page = (int64_t)pid * 2 * a.Hk + head;
             const float ks = a.scale[page], vs = a.scale[page + a.Hk];
-            scale = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
-            where = page * head_bytes + (int64_t)(at & ((1 << a.page_log) - 1)) * a.dim;
+            if (ks != ks || vs != vs) {
+              scale = make_float4(1.f, 0.f, 1.f, 0.f);
+              k_where = kNaN;
+            } else {
+              scale = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+              k_where = v_where = page * head_bytes + (int64_t)(at & ((1 << a.page_log) - 1)) * a.dim;
+            }
           }
         }
         if (st + (lane >> 3) < steps) {
           Step& step = sm.step[(st + (lane >> 3)) % kRing];
           step.scale[lane & 7] = scale;
-          step.at[lane & 7] = where;
+          step.at[0][lane & 7] = k_where;
+          step.at[1][lane & 7] = v_where;
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.plan_full[block]);

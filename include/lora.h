@@ -534,7 +534,8 @@ LORA_API lora_status lora_norm_rope(lora_dtype dtype, int T, int head_dim, int r
  *   scale    device fp32 [n_pages, 2, kv_heads] for each layer: the factor of
  *            the values of (page, k or v, head), within 2^-32 .. 2^32, or NaN.
  *            lora_cache_write makes powers of two; other factors are read as
- *            they are.
+ *            they are.  Under a factor that is a number the values of a page's
+ *            tokens must be numbers too.
  *   tables   device int32 [n_seqs, max_pages]: the pages of each sequence in
  *            order, its held ones first, -1 behind them.  One table serves all
  *            layers.
@@ -577,7 +578,8 @@ LORA_API size_t lora_cache_workspace_bytes(int n_pages, int head_dim);
  *   value  = round(x / s) to e4m3, ties to even, magnitudes past 448 to 448
  *
  * An infinity or a NaN among the new tokens makes s NaN, which turns every output
- * that reads the page's head into NaN.  Places behind the last new token are left
+ * that reads the page's head into NaN, and no other: queries before the page's
+ * tokens, or past its window, do not see it.  Places behind the last new token are left
  * as they were.  The pages must be there (lora_pages_extend), and a page that gets
  * tokens belong to one sequence alone.
  *

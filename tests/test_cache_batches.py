@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from gather_matmul_b200 import _lib, ops
-from test_cache_ops import BF16, F16, Cache, attend, gen, rows, starts_of
+from test_cache_ops import BF16, F16, Cache, attend, check_attention, gen, rows, starts_of
 from test_cache_paths import Model
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +99,56 @@ def test_a_layer_s_step_on_zeros_gives_zeros():
           torch.arange(T, device="cuda"), buf, starts_of(news))
     assert (buf[0][0] == 0).all() and (buf[0][1] == 0).all()
     assert ops.check_errors(m.work) == _lib.LORA_OK
+
+
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("news,lens,window,place", [
+    ([5, 3], [99, 40], 0, 6),                   # few rows: positions 94 and 95 come before page 6
+    ([5, 3], [101, 40], 20, 4),                 # 99 and 100 are past the window of page 4
+    ([300, 7], [300, 90], 0, 12),               # many: the first 192 rows of a prompt
+    ([300, 7], [400, 90], 64, 10),              # before the page, and past its window
+    ([1, 200], [200, 200], 0, 12),              # the other sequence's last page
+], ids=str)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_page_of_nan_spoils_only_the_queries_that_see_it(news, lens, window, place, side, dim):
+    c = Cache(lens, 2, dim, 16, seed=46)
+    q, starts = rows(sum(news), 4 * dim, BF16, gen(46)), starts_of(news)
+    y = torch.full_like(q, math.nan)
+    attend(c, q, y, news, window=window)
+    b = 0 if place * 16 < lens[0] and news[0] > 1 else 1
+    page = int(c.tables[b, place])
+    kept = c.cache.view(torch.uint8)[page, side, 1].clone(), c.scale[page, side, 1].clone()
+    c.cache.view(torch.uint8)[page, side, 1] = 0x7F
+    c.scale[page, side, 1] = math.nan
+    z = torch.full_like(q, 7.0)
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts, window=window)
+    i = lens[b] - news[b] + torch.arange(news[b], device="cuda")
+    last = torch.minimum(i, torch.tensor(place * 16 + 15, device="cuda"))
+    sees = (last >= place * 16) & ((last > i - window) if window else (i >= 0))
+    assert sees.any() and (not sees.all() or news[0] == 1)
+    first = sum(news[:b])
+    want = torch.zeros(sum(news), 4, dtype=torch.bool, device="cuda")
+    want[first:first + news[b], 2:] = sees[:, None]
+    bad = z.view(-1, 4, dim).isnan()
+    assert torch.equal(bad.any(2), want) and torch.equal(bad.all(2), want)
+    # all others are right
+    c.cache.view(torch.uint8)[page, side, 1], c.scale[page, side, 1] = kept
+    check_attention(c, q, torch.where(z.isnan(), y, z), news, window=window)
+    assert c.errors() == _lib.LORA_OK
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_a_token_of_no_number_leaves_the_tokens_before_its_page(what):
+    """Written and attended over in one step, as a prompt is."""
+    n, at, H, dim = 200, 150, 2, 128
+    c = Cache([n], H, dim, 16, seed=47)
+    x = rows(n, 2 * H * dim, BF16, gen(47))
+    q = rows(n, 4 * dim, BF16, gen(48))
+    x[at, H * dim + 3] = what                                # v of head 0
+    x[at + 20, dim + 5] = what                               # k of head 1
+    ops.cache_write(x[:, :H * dim], x[:, H * dim:], c.cache, c.scale, c.tables, c.lengths, c.work, starts=starts_of([n]))
+    y = torch.empty_like(q)
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=starts_of([n]))
+    bad = y.view(n, 4, dim).isnan()
+    assert bad[at // 16 * 16:, :2].all() and not bad[:at // 16 * 16, :2].any()
+    assert bad[(at + 20) // 16 * 16:, 2:].all() and not bad[:(at + 20) // 16 * 16, 2:].any()
