@@ -256,10 +256,10 @@ attention_few_kernel(const __grid_constant__ AttnArgs a) {
       for (int e = 0; e < 2; ++e) {
         const int row2 = 8 * nt + 2 * c + e;
         cs[nt][e] = a.c * __shfl_sync(~0u, down, (2 * c + e) * 4);
-        pos[nt][e] = row2 < t.rows ? t.len - t.n + (t.r0 + row2) / a.group : -1;
+        pos[nt][e] = row2 < t.rows ? position(a, t.len - t.n, t.r0 + row2) : -1;
       }
     }
-    const int pos_low = t.len - t.n + t.r0 / a.group, pos_high = t.len - t.n + (t.r0 + t.rows - 1) / a.group;
+    const int pos_low = position(a, t.len - t.n, t.r0), pos_high = position(a, t.len - t.n, t.r0 + t.rows - 1);
 
     float o[NT][MT][4], m[NT][2], l[NT][2];
 #pragma unroll

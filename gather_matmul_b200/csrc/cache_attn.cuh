@@ -56,6 +56,11 @@ __device__ __forceinline__ int seq_of(const AttnArgs& a, int64_t slot) {
   return lo;
 }
 
+// Position of a row's query, the sequence's first one being at `base`.  Queries before the
+// first token (more new tokens than the length) see nothing wherever they are: at -1, from
+// which any window can be taken.
+__device__ __forceinline__ int position(const AttnArgs& a, int base, int row) { return max(base + row / a.group, -1); }
+
 // units == 0: the slot holds no rows
 template <int R, int U, int C>
 __device__ __forceinline__ void tile_of(const AttnArgs& a, int b, int64_t slot, Tile& t) {
@@ -72,8 +77,7 @@ __device__ __forceinline__ void tile_of(const AttnArgs& a, int b, int64_t slot, 
   t.len = (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.M << a.page_log);
   t.r0 = (int)(at * R);
   t.rows = (int)min((int64_t)R, all - t.r0);
-  // positions of the tile's first and last query
-  const int p0 = t.len - t.n + t.r0 / a.group, p1 = t.len - t.n + (t.r0 + t.rows - 1) / a.group;
+  const int p0 = position(a, t.len - t.n, t.r0), p1 = position(a, t.len - t.n, t.r0 + t.rows - 1);
   t.hi = max(p1 + 1, 0);
   t.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), t.hi) : 0;
   t.u0 = t.lo / U;

@@ -96,7 +96,7 @@ constexpr uint32_t kFirst = 1, kLast = 2, kSecond = 4;
 // steps and results need is in the tile's own copy.
 constexpr int kItems = 2 * kRing;
 struct Item {
-  int q0, r0, rows, base;                     // row r: query q0 + r / group, at position base + r / group
+  int q0, r0, rows, base;                     // row r: query q0 + r / group; the sequence's first is at position base
   int head, tok, steps;                       // k/v head; first token and number of steps here
   int first_cta, last_cta, which;             // CTAs that share it; which of this CTA's parts it is, -1: it is whole
 };
@@ -384,9 +384,9 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       const Item& it = sm.own[tile];
       int pos, pos_low, pos_high, tok, n_steps;
       {
-        pos = 128 * tile + row < it.rows ? it.base + (it.r0 + 128 * tile + row) / a.group : -1;
-        pos_low = same(it.base + (it.r0 + 128 * tile) / a.group);
-        pos_high = same(it.base + (it.r0 + min(it.rows, 128 * tile + 128) - 1) / a.group);
+        pos = 128 * tile + row < it.rows ? position(a, it.base, it.r0 + 128 * tile + row) : -1;
+        pos_low = same(position(a, it.base, it.r0 + 128 * tile));
+        pos_high = same(position(a, it.base, it.r0 + min(it.rows, 128 * tile + 128) - 1));
         tok = same(it.tok);
         n_steps = same(it.steps);
       }
@@ -413,7 +413,8 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
           auto take = [&](int j, float* x) {
             ptx::tc_wait_ld32(reinterpret_cast<uint32_t*>(x));
             if (edge) {
-              const int hi = pos - (tok + j), lo = a.window > 0 ? hi - a.window : -1;   // visible: lo < e <= hi
+              // visible: lo < e <= hi; behind the last visible token lo may wrap, hi hides all
+              const int hi = pos - (tok + j), lo = a.window > 0 ? (int)((uint32_t)hi - (uint32_t)a.window) : -1;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (e > hi || e <= lo) x[e] = -INFINITY;

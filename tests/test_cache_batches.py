@@ -152,3 +152,18 @@ def test_a_token_of_no_number_leaves_the_tokens_before_its_page(what):
     bad = y.view(n, 4, dim).isnan()
     assert bad[at // 16 * 16:, :2].all() and not bad[:at // 16 * 16, :2].any()
     assert bad[(at + 20) // 16 * 16:, 2:].all() and not bad[:(at + 20) // 16 * 16, 2:].any()
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 40, 2 ** 30, 41, 3])
+@pytest.mark.parametrize("news,lens", [([9, 41, 200, 12], [3, 40, 150, 0]), ([7], [2]), ([300, 4], [299, 1])], ids=str)
+@pytest.mark.parametrize("dim,group", [(64, 2), (128, 1), (192, 4)])
+def test_windows_of_any_size_over_fewer_tokens_than_are_new(window, news, lens, dim, group):
+    """2^31 - 1 is a caller's "no window"; queries before the first token see nothing and get zeros."""
+    c = Cache(lens, 2, dim, 16, seed=49)
+    q = rows(sum(news), 2 * group * dim, F16, gen(49))
+    attend(c, q, torch.full_like(q, math.nan), news, window=window)
+    if window >= 2 ** 30:
+        y, z = torch.empty_like(q), torch.full_like(q, math.nan)
+        ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=starts_of(news))
+        ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts_of(news), window=window)
+        assert torch.equal(y, z)
