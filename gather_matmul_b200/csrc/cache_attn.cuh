@@ -24,6 +24,7 @@ namespace attn {
 // queries in rows q0 .. q0 + n of q, tokens [lo, hi) visible to at least one row.
 struct Tile {
   int b, q0, n, len, r0, rows, lo, hi, u0, units;   // units: with the idle ones, which come first
+  bool past;                                  // the sequence's first tile, and its length is past its table
 };
 
 // Slots of row tiles: the one of a sequence of few rows is the sequence's number, the
@@ -73,12 +74,15 @@ __device__ __forceinline__ void tile_of(const AttnArgs& a, int b, int64_t slot, 
   }
   const int64_t at = slot - slot_of<R>(a, b), all = (int64_t)t.n * a.group;
   t.units = 0;
+  t.past = false;
   if (at < 0 || at * R >= all || all < a.min_rows || all > a.max_rows) return;
-  t.len = (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.M << a.page_log);
+  t.len = max(a.lengths[b], 0);
+  const int places = a.M << a.page_log;       // tokens that the table has room for
+  t.past = at == 0 && t.len > places;
   t.r0 = (int)(at * R);
   t.rows = (int)min((int64_t)R, all - t.r0);
   const int p0 = position(a, t.len - t.n, t.r0), p1 = position(a, t.len - t.n, t.r0 + t.rows - 1);
-  t.hi = max(p1 + 1, 0);
+  t.hi = min(p1 + 1, places);                 // what lies behind the table is left out
   t.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), t.hi) : 0;
   t.u0 = t.lo / U;
   t.units = C + max((t.hi + U - 1) / U - t.u0, 1);   // one even where nothing is visible: its rows are zero
@@ -110,6 +114,7 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
     while (b + 1 < a.B && slot_of<R>(a, b + 1) <= s) ++b;
     tile_of<R, U, C>(a, b, s, t);
     mine += (unsigned long long)t.units * a.Hk;
+    if (blockIdx.x == 0 && t.past) atomicAdd(a.bad, 1);
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long in = mine;

@@ -540,7 +540,9 @@ LORA_API lora_status lora_norm_rope(lora_dtype dtype, int T, int head_dim, int r
  *            order, its held ones first, -1 behind them.  One table serves all
  *            layers.
  *   lengths  device int32 [n_seqs]: tokens of each sequence, 0 for a row that
- *            holds none.  A call that takes new tokens counts them in.
+ *            holds none.  A call that takes new tokens counts them in.  Tokens that
+ *            the sequence's row of the tables has no place for are left out, and
+ *            the sequence is counted.
  *   refs     device int32 [n_pages]: how many sequences hold each page; pages of
  *            0 are free.
  *   starts   device int32 [n_seqs + 1], 0 = starts[0] <= ... : the new tokens of

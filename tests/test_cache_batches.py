@@ -167,3 +167,43 @@ def test_windows_of_any_size_over_fewer_tokens_than_are_new(window, news, lens, 
         ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=starts_of(news))
         ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts_of(news), window=window)
         assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("past", [1, 37, 300, 2 ** 30])
+@pytest.mark.parametrize("news", [None, [2, 3], [300, 2]], ids=["single", "few", "chunks"])
+def test_a_length_past_the_table_is_counted_and_its_queries_keep_their_positions(news, past, window):
+    """The tokens behind the table are left out; the new ones are the length's last, not the table's."""
+    dim, held = 64, 320
+    c = Cache([held, 50], 2, dim, 16, seed=50, more_places=0)
+    assert c.M * 16 == held
+    T = 2 if news is None else sum(news)
+    q = rows(T, 4 * dim, BF16, gen(50))
+    y = torch.full_like(q, math.nan)
+    starts = None if news is None else starts_of(news)
+    c.lengths[0] = held + past
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, y, c.work, starts=starts, window=window)
+    assert c.errors() == _lib.LORA_ERR_BAD_INDEX and c.errors() == _lib.LORA_OK
+    n = 1 if news is None else news[0]
+    i = held + past - n + torch.arange(n, device="cuda")[:, None, None]
+    j = torch.arange(held, device="cuda")
+    seen = (j <= i) & ((j > i - window) if window else (j >= 0))
+    for h in range(2):
+        k, v = c.kv(0, h)
+        qq = q[:n, 2 * h * dim:2 * (h + 1) * dim].double().view(n, 2, dim)
+        a = (torch.einsum("ngd,jd->ngj", qq, k) * dim ** -0.5).masked_fill(~seen, -math.inf)
+        p = torch.softmax(a, -1).masked_fill(~seen.any(-1, keepdim=True), 0.0)
+        want, got = p @ v, y[:n, 2 * h * dim:2 * (h + 1) * dim].double().view(n, 2, dim)
+        # bf16 results; weights 2^-11; logits' sums, maxima and exponentials, 4 e of test_cache_ops: below 2^-10,
+        # as sum |q k| / 8 is below 20
+        tol = 2.0 ** -8 * 1.001 * want.abs() + (2.0 ** -11 + 2.0 ** -10) * (p @ v.abs()) + 2.0 ** -25
+        assert (torch.einsum("ngd,jd->ngj", qq.abs(), k.abs()) / 8).max() < 20
+        assert ((got - want).abs() <= tol).all()
+    # the other sequence is as without
+    c.lengths[0] = held
+    z = torch.full_like(q, math.nan)
+    ops.cache_attention(q, c.cache, c.scale, c.tables, c.lengths, z, c.work, starts=starts, window=window)
+    assert c.errors() == _lib.LORA_OK
+    check_attention(c, q, z, [1, 1] if news is None else news, window=window)
+    c.lens[0] = 0                                            # looked at above
+    check_attention(c, q, torch.cat([torch.zeros_like(y[:n]), y[n:]]), [1, 1] if news is None else news, window=window)
