@@ -157,7 +157,7 @@ __device__ __forceinline__ void divide(const AttnArgs& a, Shared& sm, int min_un
       while (b + 1 < a.B && slot_of<R>(a, b + 1) <= s) ++b;
       tile_of<R, U, C>(a, b, s, t);
       const unsigned long long u = (unsigned long long)t.units * a.Hk;
-      if (w0 < at + u) {
+      if (u > 0 && w0 < at + u) {             // a slot without rows has no places
         if (w0 >= at) {
           sm.slot = (int)s;
           sm.seq = b;

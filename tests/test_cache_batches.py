@@ -207,3 +207,20 @@ def test_a_length_past_the_table_is_counted_and_its_queries_keep_their_positions
     check_attention(c, q, z, [1, 1] if news is None else news, window=window)
     c.lens[0] = 0                                            # looked at above
     check_attention(c, q, torch.cat([torch.zeros_like(y[:n]), y[n:]]), [1, 1] if news is None else news, window=window)
+
+
+@pytest.mark.parametrize("new", [3, 40, 300])
+@pytest.mark.parametrize("at", ["first", "last", "between"])
+def test_sequences_without_new_tokens_have_no_places(new, at):
+    """The division among CTAs passes over them: many, with tokens of their own, around two that have new ones."""
+    none = [0] * 200
+    news = {"first": none + [new, new], "last": [new, new] + none, "between": [new] + none + [new]}[at]
+    c = Cache([900 if n else 33 for n in news], 2, 64, 16, seed=51)
+    q = rows(sum(news), 8 * 64, F16, gen(51))
+    y = torch.full_like(q, math.nan)
+    attend(c, q, y, news)
+    two = [i for i, n in enumerate(news) if n]
+    z = torch.full_like(q, math.nan)
+    ops.cache_attention(q, c.cache, c.scale, c.tables[two].contiguous(), c.lengths[two].contiguous(), z, c.work,
+                        starts=starts_of([new, new]))
+    check_attention(c, q, z, news)
