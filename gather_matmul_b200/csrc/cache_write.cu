@@ -54,6 +54,20 @@ __device__ __forceinline__ float power_scale(float a) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// With a power of two the product with 1 / s is the quotient; a page that is begun may have
+// another factor, not of lora_cache_write's making.
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+
+// the e4m3 codes of 8 elements' quotients
+template <typename E, typename F>
+__device__ __forceinline__ uint2 codes8(const uint4& x, F quotient) {
+  float f[8];
+  Elem<E>::to_f32(x, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = quotient(f[i]);
+  return make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+}
+
 // NC: 16-byte pieces (8 elements) that a lane holds of its warp's 16 tokens, at most
 template <typename E, int NC>
 __global__ void __launch_bounds__(kWThreads, NC <= 8 ? 4 : 2)
@@ -166,21 +180,20 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
     }
   }
   if (sub == 0 && lane == 0) a.scale[place] = s;
-  const float inv = 1.f / s;                                // exact: a power of two
+  const auto store = [&](auto quotient) {
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    if (k < nc) {
-      const int i = lane + 32 * k, row = i * inv_row >> 16, t = t0 + row;
-      if (t >= first && t < last) {
-        float f[8];
-        Elem<E>::to_f32(r[k], f);
-        uint2 w;
-        w.x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
-        w.y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
-        *reinterpret_cast<uint2*>(out + (int64_t)(t - page_at) * a.dim + 8 * (i - row * per_row)) = w;
+    for (int k = 0; k < NC; ++k) {
+      if (k < nc) {
+        const int i = lane + 32 * k, row = i * inv_row >> 16, t = t0 + row;
+        if (t >= first && t < last)
+          *reinterpret_cast<uint2*>(out + (int64_t)(t - page_at) * a.dim + 8 * (i - row * per_row)) = codes8<E>(r[k], quotient);
       }
     }
-  }
+  };
+  const float inv = 1.f / s;
+  // one branch for all (in each piece 17.4 us for the prompts above)
+  if (power_of_two(s)) store([=](float f) { return f * inv; });
+  else store([=](float f) { return f / s; });
 }
 
 // Single tokens: LANES lanes, of 8 elements each, for a head of k or v; little to hold
@@ -231,13 +244,9 @@ cache_write_single_kernel(const __grid_constant__ CacheWriteArgs a) {
   }
   if (lane == 0) a.scale[place] = s;
   if (8 * lane < a.dim) {
-    const float inv = 1.f / s;                              // exact: a power of two
-    float f[8];
-    Elem<E>::to_f32(r, f);
-    uint2 w;
-    w.x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
-    w.y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
-    *reinterpret_cast<uint2*>(out + (int64_t)begun * a.dim + 8 * lane) = w;
+    const float inv = 1.f / s;
+    *reinterpret_cast<uint2*>(out + (int64_t)begun * a.dim + 8 * lane) =
+        power_of_two(s) ? codes8<E>(r, [=](float f) { return f * inv; }) : codes8<E>(r, [=](float f) { return f / s; });
   }
 }
 

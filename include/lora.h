@@ -579,6 +579,7 @@ LORA_API size_t lora_cache_workspace_bytes(int n_pages, int head_dim);
  *   s      = max(s, its scale); its values become round(value * scale / s)
  *   value  = round(x / s) to e4m3, ties to even, magnitudes past 448 to 448
  *
+ * Both quotients are fp32 ones, exact but where a page's factor is no power of two.
  * An infinity or a NaN among the new tokens makes s NaN, which turns every output
  * that reads the page's head into NaN, and no other: queries before the page's
  * tokens, or past its window, do not see it.  Places behind the last new token are left

@@ -224,3 +224,35 @@ def test_sequences_without_new_tokens_have_no_places(new, at):
     ops.cache_attention(q, c.cache, c.scale, c.tables[two].contiguous(), c.lengths[two].contiguous(), z, c.work,
                         starts=starts_of([new, new]))
     check_attention(c, q, z, news)
+
+
+@pytest.mark.parametrize("news", [None, [2, 9]], ids=["single", "chunks"])
+@pytest.mark.parametrize("s", [7, 13, 15, 41, 47, 51, 55, 61, 63])
+def test_write_to_pages_begun_with_a_factor_that_is_no_power_of_two(s, news):
+    """Halfway values: s (17 .. 31) / s lies between two codes, and goes to the even one; x (1 / s) in fp32 may lie beside it."""
+    dim = 64
+    c = Cache([30, 43], 1, dim, 16, seed=52)
+    at = [int(c.tables[0, 1]), int(c.tables[1, 2])]
+    c.scale[at] = 2.0 ** -4 * s
+    old = c.cache.clone()
+    T = 2 if news is None else sum(news)
+    m = torch.arange(17, 33, 2, device="cuda").repeat(T, dim // 8).double()
+    x = (m * s / 16).to(F16)
+    x[:, 1::2] *= -1
+    assert torch.equal(x.double().abs(), m * s / 16)
+    ops.cache_write(x, x, c.cache, c.scale, c.tables, c.lengths, c.work, starts=None if news is None else starts_of(news))
+    assert (c.scale[at] == 2.0 ** -4 * s).all()
+    # m = 16 + 2 i + 1 lies between 16 + 2 i and 16 + 2 i + 2: the multiple of 4
+    want = torch.where(m % 4 == 1, m - 1, m + 1)
+    want[:, 1::2] *= -1
+    t = 0
+    for b, n in enumerate([1, 1] if news is None else news):
+        first = c.lens[b] - n
+        for k in range(n):
+            page, place = int(c.tables[b, (first + k) // 16]), (first + k) % 16
+            if page == at[b]:
+                assert torch.equal(c.cache[page, :, 0, place].double(), want[t + k].expand(2, dim)), (b, k)
+        begun = first % 16
+        assert torch.equal(c.cache.view(torch.uint8)[at[b], :, :, :begun], old.view(torch.uint8)[at[b], :, :, :begun])
+        t += n
+    assert c.errors() == _lib.LORA_OK
