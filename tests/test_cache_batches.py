@@ -256,3 +256,17 @@ def test_write_to_pages_begun_with_a_factor_that_is_no_power_of_two(s, news):
         assert torch.equal(c.cache.view(torch.uint8)[at[b], :, :, :begun], old.view(torch.uint8)[at[b], :, :, :begun])
         t += n
     assert c.errors() == _lib.LORA_OK
+
+
+def test_extend_counts_lengths_past_their_tables_whatever_they_add_up_to():
+    """64 sequences that lack 2^26 places each: 2^32 in all."""
+    B, M, page = 64, 4, 16
+    tables = torch.full((B, M), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(B * M, dtype=torch.int32, device="cuda")
+    lengths = torch.full((B,), ((1 << 26) + M) * page, dtype=torch.int32, device="cuda")
+    work = ops.cache_workspace(B * M, 64)
+    ops.pages_extend(tables, lengths, refs, page, work)
+    assert torch.equal(tables.flatten(), torch.arange(B * M, dtype=torch.int32, device="cuda")) and (refs == 1).all()
+    assert ops.check_errors(work) == _lib.LORA_ERR_BAD_INDEX
+    ops.pages_extend(tables, lengths, refs, page, work)
+    assert ops.check_errors(work) == _lib.LORA_ERR_BAD_INDEX
