@@ -1,7 +1,6 @@
 // extern "C" entry points of the paged 8-bit key/value cache: host-side
 // argument checks and dispatch.  See include/lora.h for the contract of each call.
 #include <limits.h>
-#include <math.h>
 
 #include "cache.h"
 #include "common.cuh"
@@ -137,7 +136,8 @@ lora_status lora_cache_attention(lora_dtype dtype, int T, int n_seqs, int q_head
                                  size_t work_bytes, lora_stream_t stream) {
   if ((dtype != LORA_F16 && dtype != LORA_BF16) || T < 0 || q_heads <= 0 || window < 0)
     return LORA_ERR_INVALID_ARG;
-  if (!isfinite(softmax_scale) || softmax_scale <= 0.f) return LORA_ERR_INVALID_ARG;
+  // its product with log2 e is a number too
+  if (!(softmax_scale > 0.f && softmax_scale < 0x1p127f)) return LORA_ERR_INVALID_ARG;
   TRY(check_cache(n_pages, kv_heads, page_tokens, head_dim));
   TRY(check_seqs(n_seqs, max_pages));
   if (q_heads > LORA_MAX_HEADS || T > LORA_MAX_TOKENS || (int64_t)T * q_heads > INT_MAX / 2)

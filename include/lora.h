@@ -612,7 +612,7 @@ LORA_API lora_status lora_cache_write(lora_dtype dtype, int T, int n_seqs, int k
  *   q, y     device [T, ldq], [T, ldy] dtype, q_heads heads side by side, 16-byte
  *            aligned, strides multiples of 8; they may be columns of one matrix,
  *            not the same ones.
- *   softmax_scale  > 0, finite (1 / sqrt(head_dim) as a rule).
+ *   softmax_scale  > 0, below 2^127 (1 / sqrt(head_dim) as a rule).
  *   window   0: every earlier token is visible.
  * q_heads a multiple of kv_heads, at most LORA_MAX_HEADS; T * q_heads < 2^30.
  */
