@@ -270,3 +270,15 @@ def test_extend_counts_lengths_past_their_tables_whatever_they_add_up_to():
     assert ops.check_errors(work) == _lib.LORA_ERR_BAD_INDEX
     ops.pages_extend(tables, lengths, refs, page, work)
     assert ops.check_errors(work) == _lib.LORA_ERR_BAD_INDEX
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (80, BF16), (128, F16), (256, BF16)])
+@pytest.mark.parametrize("news", [None, [3, 2], [40, 60], [1, 300]], ids=["single", "few", "chunks", "mixed"])
+def test_any_factors_in_both_kernels(news, dim, dtype):
+    """Factors that are no powers of two, of k and of v, over a range of 2^20."""
+    c = Cache([600, 301], 2, dim, 16, seed=53, scales=(-16, 4))
+    c.scale *= torch.rand(c.scale.shape, generator=gen(53), device="cuda") + 0.5
+    c.scale[:, 0] = (c.scale[:, 0].log2() / 4 - 6).exp2()     # logits of moderate size
+    q = rows(2 if news is None else sum(news), 6 * dim, dtype, gen(54))
+    attend(c, q, torch.full_like(q, math.nan), news)
+    attend(c, q, torch.full_like(q, math.nan), news, window=100)
