@@ -104,7 +104,7 @@ struct Item {
 struct ManyShared {
   Shared div;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], o_empty[2], plan_items[kBlocks], plan_full[kBlocks], plan_empty[kBlocks], done[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], o_empty[2], plan_items[kBlocks], plan_full[kBlocks], plan_empty[kBlocks], meet[2], done[2];
   uint32_t tmem;
   int stop;
   int flag[2];
@@ -206,11 +206,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) ptx::mbar_arrive(bar);
 }
 
-// the threads of a tile
-__device__ __forceinline__ void tile_sync(int tile) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + tile) : "memory");
-}
-
 // Sums of a tile's row that several CTAs share: [which][tile]: [D / 4][128] of
 // four values, then [128] of (maximum, sum).
 template <int D>
@@ -253,11 +248,22 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       ptx::mbar_init(&sm.plan_full[i], 1);
       ptx::mbar_init(&sm.plan_empty[i], 4 * (M::kTiles + 2) + M::kTiles);   // softmax and conversion, issuing warps
     }
-    ptx::mbar_init(&sm.done[0], 1);
-    ptx::mbar_init(&sm.done[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.meet[i], 4);
+      ptx::mbar_init(&sm.done[i], 1);
+    }
     sm.stop = 0;
     ptx::fence_mbar_init();
   }
+  // Waits that give up let everyone run on, with plans that may be another step's: loops
+  // end all the same, nothing is read or written where these plans say, and a call that
+  // met this is counted (its workspace is then to be filled with zeros again).
+  if (tid < kRing) {
+    for (int i = 0; i < 16; ++i) sm.step[tid].at[i / 8][i % 8] = kNowhere;
+    sm.step[tid].item = 0;
+    sm.step[tid].flags = 0;
+  }
+  if (tid < kItems) sm.item[tid] = {0, 0, 0, 0, 0, 0, 1, 0, 0, -1};
   ptx::grid_dep_wait();
   ptx::grid_dep_launch_dependents();
   ptx::tc_fence_before();
@@ -276,7 +282,13 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t S = tmem + lanes + s_col + tile * kN, O = tmem + lanes + o_col + tile * D;
     float cs = 0.f;
-    int st = 0, n_s = 0;
+    int st = 0, n_s = 0, met = 0;
+    // the threads of a tile, as a barrier that a wait can leave
+    auto tile_sync = [&]() {
+      warp_arrive(&sm.meet[tile], lane);
+      ptx::mbar_wait_asm(ptx::smem_u32(&sm.meet[tile]), met & 1, stop);
+      ++met;
+    };
     auto planned = [&]() {
       ptx::mbar_wait_asm(ptx::smem_u32(&sm.plan_full[st / kBlock % kBlocks]), (st / kRing) & 1, stop);
     };
@@ -290,7 +302,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
         ptx::mbar_wait_asm(ptx::smem_u32(&sm.plan_items[st / kBlock % kBlocks]), (st / kRing) & 1, stop);
         const int item = same(sm.step[st % kRing].item);
         if (same(sm.item[item].rows) > 128 * tile) return item;
-        for (int n = same(sm.item[item].steps); n > 0; --n) {
+        for (int n = same(sm.item[item].steps); n > 0 && st < steps; --n) {
           planned();
           pass();
         }
@@ -309,7 +321,9 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
     };
     auto walk = [&](const Item& it) -> Walk {
       const int k = 128 * tile + tt / kLanes, r = it.r0 + k;
-      return {it.q0 + r / a.group, r % a.group, 8 * piece < a.dim ? it.rows - k : 0};
+      const Walk w = {it.q0 + r / a.group, r % a.group, 8 * piece < a.dim ? it.rows - k : 0};
+      __threadfence_block();                  // the item has been read
+      return *const_cast<volatile int*>(&sm.stop) ? Walk{0, 0, 0} : w;
     };
     auto place = [&](const Item& it, const Walk& w, int64_t ld) -> int64_t {
       return (int64_t)w.line * ld + (it.head * a.group + w.head) * a.dim + 8 * piece;
@@ -368,7 +382,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       }
       if (row == 0) sm.own[tile] = sm.item[item];
       ptx::fence_proxy_async_smem();
-      tile_sync(tile);
+      tile_sync();
       // The factor of a score is a page's (at least 2^-32) times this one.  It stays off zero,
       // since masked scores are -inf before it: a row of zeros has the scale 2^-120.  Where
       // the bound is met the scores are below 2^-30, and no weight changes.
@@ -554,13 +568,13 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
         ptx::tc_fence_before();
         warp_arrive(&sm.o_empty[tile], lane);
         __threadfence();
-        tile_sync(tile);
+        tile_sync();
         if (row == 0) {
           int* join = a.join + 2 * first_cta + tile;
           sm.flag[tile] = atomicAdd(join, 1) == last_cta - first_cta;
           if (sm.flag[tile]) *join = 0;                   // as the next call finds it
         }
-        tile_sync(tile);
+        tile_sync();
         out = same(sm.flag[tile]);
         if (out) {
           __threadfence();
@@ -592,12 +606,12 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
       if (out) {
-        tile_sync(tile);
+        tile_sync();
         Walk w = walk(it);
 #pragma unroll 1
         for (int k = tt / kLanes; k < 128 && w.left > 0; k += kApart, on(w))
           *reinterpret_cast<uint4*>(static_cast<E*>(a.y) + place(it, w, a.ldy)) = *chunk(k, piece);
-        tile_sync(tile);
+        tile_sync();
       }
       if (item >= 0) put_q(item);
     }
@@ -771,7 +785,7 @@ attention_many_kernel(const __grid_constant__ AttnArgs a) {
       }
       // nothing is in flight when tensor memory goes back
       commit(&sm.done[t]);
-      ptx::mbar_wait_asm(ptx::smem_u32(&sm.done[t]), 0, stop);
+      ptx::mbar_wait(&sm.done[t], 0);         // whatever other waits did
     };
     if (role < M::kTiles) {
       if (role == 0) issue(std::integral_constant<int, 0>{});
