@@ -184,12 +184,16 @@ lora_status lora_cache_attention(lora_dtype dtype, int T, int n_seqs, int q_head
   a.c = (float)((double)softmax_scale * 1.4426950408889634);
   cudaGetLastError();
   // Sequences of up to kFewRows rows and others have kernels of their own; only the device
-  // knows them where starts is given.  The kernel for many rows takes all, at less than
-  // half the speed for few; a second launch costs 20 us, most of it the kernel's way to
-  // its first products.  Items (sequences x k/v heads) are what the host knows:
+  // knows them where starts is given.  The kernel for many rows takes all, slower for few
+  // (at half the speed where there is much to read); a second launch costs up to 20 us, most
+  // of it the kernel's way to its first products.  Items (sequences x k/v heads) are what
+  // the host knows:
   //   up to 128, one for each CTA at most: one kernel.  12 sequences of up to 8 tokens over
-  //     12 000 on 4 heads 43 us, in two kernels 75; 16 of up to 200 over 2000 38 and 60;
-  //     36 of up to 4 over 30 000 (144 items) 99 and 91
+  //     12 000 on 4 heads 43 us, in two kernels 75; 16 of up to 200 over 2000 38 and 60; 16
+  //     of up to 8 over 16 000 on 8 heads 66 and 91.  It loses where all have one or two
+  //     tokens: 16 over 16 000 on 8 heads 66 and 56, 8 over 30 000 51 and 42, 4 over 2000
+  //     21 and 24; 128 over 8000 on 1 head 53 and 56; 36 of up to 4 over 30 000 on 4 heads
+  //     (144 items) 99 and 91
   //   up to 8 for each CTA: one, unless the rows say that most sequences are short.  64 of
   //     up to 200 over 8000 94 us and 122; 64 of up to 4 over 8000 66 and 61
   //   more: two.  300 of up to 16 over 8000 on 8 heads 326 us and 305; 150 of up to 64

@@ -19,9 +19,14 @@
 // products have just read.  q's rows are brought to fp16 by powers of two (their largest
 // elements to 2^7 .. 2^8), which costs less than the rounding of the sums.
 //
-// 128 sequences of 4096 tokens, 32 heads on 8 of 128: 198 us, 5.4 TB/s, 0.83 of the
-// measured copy rate; 512 ragged ones of up to 8192: 227 us, 0.75 (through stages in
-// shared memory, by cp.async: 407 before the idle units below, 352 in registers).
+// 128 sequences of 4096 tokens, 32 heads on 8 of 128: 200 us, 5.4 TB/s, 0.82 of the
+// measured copy rate; 512 ragged ones of up to 8192: 231 us, 0.74 (through stages in
+// shared memory, by cp.async: 407 before the idle units below, 352 in registers).  Between
+// two items of a CTA (about seven of the ragged batch) loads stop, until the warps' sums
+// have met and the next item's pages are known.  9 to 16 rows spill registers (280 bytes of
+// a thread at heads of 128, 640 at 256) and are not bound by memory: 128 heads on 8 over
+// the same 128 sequences 292 us, 0.56; over 64, heads of 256, 128 on 8 410 us, 0.40, where
+// 64 on 8 take 217, 0.75.
 #include <cfloat>
 
 #include "cache_attn.cuh"

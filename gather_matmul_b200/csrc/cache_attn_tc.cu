@@ -5,8 +5,9 @@
 // Products run on tcgen05: S = Q K^T into tensor memory, the weights P back into
 // tensor memory as fp16, O += P V with P from there.  A CTA holds two tiles of 128
 // rows (one for heads of more than 128 elements), so that k and v are converted once
-// for 256 rows; as fp16 operands q, k and v keep all their bits.  It goes through its
-// items in steps of 128 tokens:
+// for 256 rows; as fp16 operands k and v keep all their bits, and q, whose rows a power of
+// two brings to 2^7 .. 2^8, what is above 2^-32 of the row's largest element.  It goes
+// through its items in steps of 128 tokens:
 //
 //   a warpgroup for each tile's softmax, a thread for each row: scores of 64 tokens
 //     from tensor memory, their weights back, the running sums; the products of one
@@ -17,10 +18,13 @@
 //   a warp for each tile that issues its products, and one that plans: it looks up
 //     pages and scales of the next steps, four steps at a time, and divides the items
 //
-// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1100 us, 937 TFLOP/s,
-// 0.57 of the measured rate of a 16-bit product (a CTA's step 4800 cycles at two tiles).
-// No unit is full: the tensor pipe is busy 53 % of the time, issue slots 51 %, special
-// functions 32 %.  Scores are there before the softmax asks for them; it forms the
+// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1200 us in a loop of calls,
+// 860 TFLOP/s, 0.53 of the measured rate of a 16-bit product, at the clock that the power
+// limit leaves; 1090 us, 0.58, where calls lie apart (a CTA's step 4800 cycles at two
+// tiles).  4 x 1024 queries behind 3072, apart: 32 heads of 128 on 8 307 us, 0.48, on 32
+// 319 us, 0.46; with one tile and one buffer of k and v, 32 heads of 192 on 8 521 us, 0.42,
+// 16 of 256 on 4 387 us, 0.38.  No unit is full: the tensor pipe is busy 53 % of the time, issue slots 54 %, special
+// functions 33 %.  Scores are there before the softmax asks for them; it forms the
 // weights of 64 tokens in 1250 cycles alone and in up to 2800 beside the other tile's,
 // most of it waiting for shared and tensor memory, which the operands of the products
 // (q and k 1536 cycles of a step, v 512, at 128 bytes a cycle), the converted tiles

@@ -10,9 +10,10 @@
 // Several tokens: one warp holds 16 tokens of one head of k or v in registers (read
 // once), page / 16 warps meet in shared memory for the maximum.  Bound by memory, two
 // bytes read and one written for each element, and by the chain from a slot to its
-// sequence, its page and its scale, which values are loaded beside.  8 x 1024 tokens of
-// 8 heads of 128: 16 us, 3.2 TB/s, 0.48 of the measured copy rate (three CTAs to an SM
-// instead of four 18).  512 single tokens 4.7 us; in the kernel of several 15.
+// sequence, its page and its scale, which values are loaded beside, and which each of two
+// waves of CTAs pays.  8 x 1024 tokens of 8 heads of 128: 15.3 us, 3.3 TB/s, 0.50 of the
+// measured copy rate (three CTAs to an SM instead of four 18).  512 single tokens 5 us; in
+// the kernel of several 15.
 #include "cache.h"
 #include "common.cuh"
 #include "internal.h"
@@ -191,7 +192,7 @@ cache_write_kernel(const __grid_constant__ CacheWriteArgs a) {
     }
   };
   const float inv = 1.f / s;
-  // one branch for all (in each piece 17.4 us for the prompts above)
+  // one branch for all (a branch in each piece 17.4 us)
   if (power_of_two(s)) store([=](float f) { return f * inv; });
   else store([=](float f) { return f / s; });
 }

@@ -604,8 +604,9 @@ LORA_API lora_status lora_cache_write(lora_dtype dtype, int T, int n_seqs, int k
  *
  *   p_j = exp(softmax_scale q . k_j) / sum over the visible j,   y = sum_j p_j v_j
  *
- * with sums and softmax in fp32, q in full, the weights p rounded to 11 bits, and
- * one rounding to dtype.  A query that sees nothing (a row of length 0, more new
+ * with sums and softmax in fp32, exponentials to within 2^-18 of their value, q to
+ * within 2^-32 of its head's largest element (where that is at least 2^-113), the
+ * weights p rounded to 11 bits, and one rounding to dtype.  A query that sees nothing (a row of length 0, more new
  * tokens than the length) gets zeros; the tokens of a missing page are left out.
  * Head h reads k/v head h / (q_heads / kv_heads).
  *
