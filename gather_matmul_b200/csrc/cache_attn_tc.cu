@@ -21,17 +21,18 @@
 // 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1200 us in a loop of calls,
 // 860 TFLOP/s, 0.53 of the measured rate of a 16-bit product, at the clock that the power
 // limit leaves; 1090 us, 0.58, where calls lie apart (a CTA's step 4800 cycles at two
-// tiles).  4 x 1024 queries behind 3072, apart: 32 heads of 128 on 8 307 us, 0.48, on 32
-// 319 us, 0.46; with one tile and one buffer of k and v, 32 heads of 192 on 8 521 us, 0.42,
-// 16 of 256 on 4 387 us, 0.38.  No unit is full: the tensor pipe is busy 53 % of the time,
-// issue slots 54 %, special functions 33 %.  Scores are there before the softmax asks for
-// them; it forms the weights of 64 tokens in 1250 cycles alone and in up to 2800 beside the
-// other tile's, most of it waiting for shared and tensor memory, which the operands of the products
-// (q and k 1536 cycles of a step, v 512, at 128 bytes a cycle), the converted tiles
-// (512) and the scores and weights themselves keep busy.  Measured otherwise: one
-// warpgroup that converts k, then v 1310; scores of 128 tokens at once, which have room
-// for one buffer, 1235; q as an operand from tensor memory, which leaves room for one
-// buffer of 64, 1370; two softmax warpgroups a tile, half of the columns each, 1255.
+// tiles).  4 x 1024 queries, each the last of 4096 tokens, apart: 32 heads of 128 on 8 307
+// us, 0.48, on 32 319 us, 0.46; with one tile and one buffer of k and v, 32 heads of 192
+// on 8 521 us, 0.42, 16 of 256 on 4 387 us, 0.38.  No unit is full: the tensor pipe is
+// busy 53 % of the time, issue slots 54 %, special functions 33 %. Scores are there
+// before the softmax asks for them; it forms the weights of 64 tokens in 1250 cycles
+// alone and in up to 2800 beside the other tile's, most of it waiting for shared and
+// tensor memory, which the operands of the products (q and k 1536 cycles of a step, v
+// 512, at 128 bytes a cycle), the converted tiles (512) and the scores and weights
+// themselves keep busy.  Measured otherwise: one warpgroup that converts k, then v 1310;
+// scores of 128 tokens at once, which have room for one buffer, 1235; q as an operand
+// from tensor memory, which leaves room for one buffer of 64, 1370; two softmax
+// warpgroups a tile, half of the columns each, 1255.
 #include <cfloat>
 #include <type_traits>
 
