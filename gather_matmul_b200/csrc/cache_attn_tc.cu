@@ -18,9 +18,9 @@
 //   a warp for each tile that issues its products, and one that plans: it looks up
 //     pages and scales of the next steps, four steps at a time, and divides the items
 //
-// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1200 us in a loop of calls,
-// 860 TFLOP/s, 0.53 of the measured rate of a 16-bit product, at the clock that the power
-// limit leaves; 1090 us, 0.58, where calls lie apart (a CTA's step 4800 cycles at two
+// 8 x 1024 queries of 32 heads of 128 behind 7168 tokens each: 1200 to 1230 us in a loop of
+// calls, 850 TFLOP/s, 0.52 of the measured rate of a 16-bit product, at the clock that the
+// power limit leaves; 1090 us, 0.58, where calls lie apart (a CTA's step 4800 cycles at two
 // tiles).  4 x 1024 queries, each the last of 4096 tokens, apart: 32 heads of 128 on 8 307
 // us, 0.48, on 32 319 us, 0.46; with one tile and one buffer of k and v, 32 heads of 192
 // on 8 521 us, 0.42, 16 of 256 on 4 387 us, 0.38.  No unit is full: the tensor pipe is
